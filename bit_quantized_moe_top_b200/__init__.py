@@ -23,6 +23,7 @@ FMT_INT_ASYM, FMT_BITPLANE_LUT, FMT_DENSE16 = 0, 1, 2
 FLAG_NO_TOPK_RENORM = 1
 FLAG_DETERMINISTIC = 2
 PATH_AUTO, PATH_DECODE, PATH_PREFILL = 0, 1, 2
+BF16, FP16, FP32 = 0, 1, 2
 
 # every symbol the header declares
 EXPORTS = ["moe_layer_create", "moe_layer_set_expert_weights", "moe_layer_set_bits", "moe_layer_set_comp_top_n",
@@ -32,6 +33,8 @@ EXPORTS = ["moe_layer_create", "moe_layer_set_expert_weights", "moe_layer_set_bi
            "moe_layer_kernel_times", "moe_route_topk_noalloc", "moe_plan_reduce", "moe_plan_restore",
            "moe_layer_release_planes", "moe_layer_reload_planes", "moe_layer_page_state",
            "moe_layer_set_tileq", "moe_layer_clear_tileq",
+           "moe_block_norm", "moe_quantize_rows", "moe_int8_matmul", "moe_grouped_matmul", "moe_op_sync_status",
+           "moe_op_set_wait_limit",
            "moe_status_string", "moe_layer_destroy"]
 
 
@@ -51,6 +54,19 @@ class PlanBlock(ctypes.Structure):
     _fields_ = [("committed_bits", ctypes.c_int), ("floor_bits", ctypes.c_int), ("max_steps", ctypes.c_int),
                 ("plane_bytes", ctypes.c_longlong), ("sensitivity", ctypes.c_float * 5),
                 ("routing_mult", ctypes.c_float), ("prompt_factor", ctypes.c_float)]
+
+
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int), ("width", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("residual_dtype", ctypes.c_int), ("branch", ctypes.c_void_p), ("branch_stride", ctypes.c_longlong),
+                ("branch_rows", ctypes.c_int), ("pairs", ctypes.c_int), ("inv_pos", ctypes.c_void_p),
+                ("pair_weights", ctypes.c_void_p), ("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("gate_token_stride", ctypes.c_longlong), ("gate_channel_stride", ctypes.c_int),
+                ("gate_sigmoid", ctypes.c_int), ("residual", ctypes.c_void_p),
+                ("residual_stride", ctypes.c_longlong), ("residual_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float), ("pre_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("residual_out", ctypes.c_void_p),
+                ("residual_out_stride", ctypes.c_longlong), ("h", ctypes.c_void_p), ("h_stride", ctypes.c_longlong)]
 
 
 _LIB = None
@@ -87,6 +103,13 @@ def _lib() -> ctypes.CDLL:
         IP, LP = ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_longlong)
         lib.moe_plan_reduce.argtypes = [PB, I, ctypes.c_longlong, ctypes.c_float, IP, LP]
         lib.moe_plan_restore.argtypes = [PB, I, IP, ctypes.c_longlong, ctypes.c_float, IP, LP]
+        LL = ctypes.c_longlong
+        lib.moe_block_norm.argtypes = [ctypes.POINTER(BlockNormArgs), P]
+        lib.moe_quantize_rows.argtypes = [P, LL, I, I, P, I, I, P, LL, P, P]
+        lib.moe_int8_matmul.argtypes = [P, LL, P, P, LL, LL, P, P, I, I, I, I, P, LL, I, P]
+        lib.moe_grouped_matmul.argtypes = [P, LL, P, LL, LL, P, I, I, I, I, I, P, LL, I, P]
+        lib.moe_op_sync_status.argtypes = [P]
+        lib.moe_op_set_wait_limit.argtypes = [ctypes.c_ulonglong]
         lib.moe_status_string.argtypes = [I]
         lib.moe_status_string.restype = ctypes.c_char_p
         lib.moe_layer_destroy.argtypes = [P]
@@ -287,6 +310,209 @@ def moe_status_string(status: int) -> str:
 
 def moe_layer_destroy(layer: int) -> None:
     _lib().moe_layer_destroy(layer)
+
+
+# ---------------------------------------------------------------------------
+# stand-alone operators around the experts
+# ---------------------------------------------------------------------------
+
+def _require(ok, where: str):
+    if not ok:
+        raise MoEError(1, where)
+
+
+_DTYPES = {}
+
+
+def _dtype(t) -> int:
+    """The library's code of a torch dtype, or -1."""
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
+    return _DTYPES.get(t, -1)
+
+
+def _call(device, stream, where: str, fn, *args) -> None:
+    """fn(*args, stream) with ``device`` current, on its current stream unless one is given."""
+    import torch
+    index = device.index
+    if stream is None:
+        stream = torch.cuda.current_stream(index).cuda_stream
+    if index == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != MOE_OK:
+        raise MoEError(status, where)
+
+
+def _rows(t, where: str, device, n=None, width=None) -> int:
+    """Row stride of a 2-D tensor whose rows are contiguous; checks shape and device."""
+    _require(t.dim() == 2 and t.device == device and (t.stride(1) == 1 or t.shape[1] == 1), where)
+    _require((n is None or t.shape[0] == n) and (width is None or t.shape[1] == width), where)
+    return t.stride(0)
+
+
+def _flat(t, where: str, device, dtype, *shape) -> None:
+    _require(t.device == device and t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous(), where)
+
+
+def moe_block_norm(residual=None, branch=None, *, w_pre=None, w_post=None, gate=None, gate_sigmoid: bool = False,
+                   residual_scale: float = 1.0, branch_scale: float = 1.0, eps: float = 1e-6,
+                   weight_offset: float = 0.0, inv_pos=None, pair_weights=None, residual_out=None, h_out=None,
+                   stream: Optional[int] = None):
+    """Norms before and after a block with its gate, residual scale and the
+    combination of the experts' rows; returns (residual_out, h).
+
+    residual [T, K]; branch [T, K], or the experts' rows [R, K] with inv_pos
+    int32 [T, k] and pair_weights fp32 [T, k]; w_post, w_pre [K]; gate [K] (per
+    channel), [T, 1] (per token) or [T, K]. Without w_pre no h is made; without
+    a branch no residual_out is made unless one is given. residual_out may be
+    ``residual`` itself."""
+    import torch
+    f = "moe_block_norm"
+    _require(residual is not None or branch is not None, f)
+    lead = residual if residual is not None else branch
+    device = lead.device
+    _require(lead.is_cuda and lead.dim() == 2, f)
+    K = lead.shape[1]
+    if residual is not None:
+        T = residual.shape[0]
+    else:
+        T = branch.shape[0] if inv_pos is None else inv_pos.shape[0]
+    if branch is not None:
+        dt = branch.dtype
+    elif w_pre is not None:
+        dt = w_pre.dtype
+    else:
+        dt = residual.dtype
+    if residual_out is None and branch is not None:
+        residual_out = torch.empty((T, K), dtype=dt if residual is None else residual.dtype, device=device)
+    if h_out is None and w_pre is not None:
+        h_out = torch.empty((T, K), dtype=dt, device=device)
+    a = BlockNormArgs(tokens=T, width=K, dtype=_dtype(dt), residual_scale=residual_scale, branch_scale=branch_scale,
+                      eps=eps, weight_offset=weight_offset, gate_sigmoid=1 if gate_sigmoid else 0)
+    rdt = residual.dtype if residual is not None else (residual_out.dtype if residual_out is not None else dt)
+    a.residual_dtype = _dtype(rdt)
+    if residual is not None:
+        a.residual, a.residual_stride = residual.data_ptr(), _rows(residual, f, device)
+    if branch is not None:
+        a.branch_stride = _rows(branch, f, device, None if inv_pos is not None else T, K)
+        a.branch, a.branch_rows = branch.data_ptr(), branch.shape[0]
+    if inv_pos is not None or pair_weights is not None:
+        _require(inv_pos is not None and pair_weights is not None and inv_pos.dim() == 2, f)
+        k = inv_pos.shape[1]
+        _flat(inv_pos, f, device, torch.int32, T, k)
+        _flat(pair_weights, f, device, torch.float32, T, k)
+        _require(k >= 1, f)
+        a.inv_pos, a.pair_weights, a.pairs = inv_pos.data_ptr(), pair_weights.data_ptr(), k
+    if w_post is not None:
+        _flat(w_post, f, device, dt, K)
+        a.post_weight = w_post.data_ptr()
+    if w_pre is not None:
+        _flat(w_pre, f, device, dt, K)
+        a.pre_weight = w_pre.data_ptr()
+    if gate is not None:
+        _require(gate.device == device and gate.dtype == dt, f)
+        if gate.dim() == 1:
+            _flat(gate, f, device, dt, K)
+            a.gate_token_stride, a.gate_channel_stride = 0, 1
+        else:
+            _require(gate.dim() == 2 and gate.shape[0] == T and gate.shape[1] in (1, K), f)
+            a.gate_channel_stride = 0 if gate.shape[1] == 1 else 1
+            _require(a.gate_channel_stride == 0 or gate.stride(1) == 1, f)
+            a.gate_token_stride = gate.stride(0)
+        a.gate = gate.data_ptr()
+    if residual_out is not None:
+        _require(residual_out.dtype == rdt, f)
+        a.residual_out, a.residual_out_stride = residual_out.data_ptr(), _rows(residual_out, f, device, T, K)
+    if h_out is not None:
+        _require(h_out.dtype == dt, f)
+        a.h, a.h_stride = h_out.data_ptr(), _rows(h_out, f, device, T, K)
+    if T > 0:
+        _call(device, stream, f, _lib().moe_block_norm, ctypes.byref(a))
+    return residual_out, h_out
+
+
+def moe_quantize_rows(x, src_rows=None, codes=None, scales=None, stream: Optional[int] = None):
+    """Rows of x (bf16 or fp16 [M, K]), or the rows src_rows (int32 [R]) selects,
+    as 8-bit codes with one scale each; returns (codes int8 [R, K], scales fp32 [R])."""
+    import torch
+    f = "moe_quantize_rows"
+    _require(x.is_cuda, f)
+    ldx = _rows(x, f, x.device)
+    M, K = x.shape
+    R = M
+    if src_rows is not None:
+        R = src_rows.shape[0]
+        _flat(src_rows, f, x.device, torch.int32, R)
+    if codes is None:
+        codes = torch.empty((R, K), dtype=torch.int8, device=x.device)
+    if scales is None:
+        scales = torch.empty((R,), dtype=torch.float32, device=x.device)
+    _require(codes.dtype == torch.int8, f)
+    _flat(scales, f, x.device, torch.float32, R)
+    _call(x.device, stream, f, _lib().moe_quantize_rows, x.data_ptr(), ldx, M, _dtype(x.dtype), _ptr(src_rows), R, K,
+          codes.data_ptr(), _rows(codes, f, x.device, R, K), scales.data_ptr())
+    return codes, scales
+
+
+def _product(f, x, w, offsets, out_dtype, out):
+    """Checks of the grouped products: (row stride, weight strides, E, K, N, out)."""
+    import torch
+    _require(x.is_cuda and w.dtype == x.dtype and w.device == x.device, f)
+    ldx = _rows(x, f, x.device)
+    R, K = x.shape
+    if w.dim() == 2:
+        w = w.unsqueeze(0)
+    _require(w.dim() == 3 and w.shape[2] == K and (w.stride(2) == 1 or K == 1), f)
+    E, N = w.shape[0], w.shape[1]
+    if offsets is not None:
+        _flat(offsets, f, x.device, torch.int32, E + 1)
+    if out is None:
+        out = torch.empty((R, N), dtype=out_dtype, device=x.device)
+    _require(out_dtype is None or out.dtype == out_dtype, f)
+    return ldx, w.stride(1), w.stride(0), R, E, K, N, out, _rows(out, f, x.device, R, N)
+
+
+def moe_int8_matmul(x, row_scales, w, channel_scales, offsets=None, out_dtype=None, out=None,
+                    stream: Optional[int] = None):
+    """y[r, n] = row_scales[r] * channel_scales[e, n] * sum_k x[r, k] w[e, n, k]
+    of int8 codes x [R, K] and w [N, K] or [E, N, K] (channel_scales [N] or
+    [E, N]), e the expert whose range offsets[e] <= r < offsets[e + 1] holds r
+    (int32 [E + 1] on the device; None: one matrix for all rows). Rows in no
+    range are left as they were. out_dtype: bf16 (default), fp16 or fp32."""
+    import torch
+    f = "moe_int8_matmul"
+    _require(x.dtype == torch.int8, f)
+    ldx, ldw, ldwe, R, E, K, N, out, ldy = _product(f, x, w, offsets, out_dtype or (torch.bfloat16 if out is None else None),
+                                                    out)
+    _flat(row_scales, f, x.device, torch.float32, R)
+    _require(channel_scales.numel() == E * N, f)
+    _flat(channel_scales, f, x.device, torch.float32, *w.shape[:-1])
+    _call(x.device, stream, f, _lib().moe_int8_matmul, x.data_ptr(), ldx, row_scales.data_ptr(), w.data_ptr(), ldw,
+          ldwe, channel_scales.data_ptr(), _ptr(offsets), R, E, K, N, out.data_ptr(), ldy, _dtype(out.dtype))
+    return out
+
+
+def moe_grouped_matmul(x, w, offsets=None, out_dtype=None, out=None, stream: Optional[int] = None):
+    """y[r, n] = sum_k x[r, k] w[e, n, k] of bf16 or fp16 rows x [R, K] in expert
+    order and experts w [E, N, K] (or [N, K]); offsets as for moe_int8_matmul.
+    out_dtype: bf16, fp16 or fp32 (default: x's)."""
+    f = "moe_grouped_matmul"
+    ldx, ldw, ldwe, R, E, K, N, out, ldy = _product(f, x, w, offsets, out_dtype or (x.dtype if out is None else None), out)
+    _call(x.device, stream, f, _lib().moe_grouped_matmul, x.data_ptr(), ldx, w.data_ptr(), ldw, ldwe, _ptr(offsets), R,
+          E, K, N, _dtype(x.dtype), out.data_ptr(), ldy, _dtype(out.dtype))
+    return out
+
+
+def moe_op_sync_status(stream: Optional[int] = None) -> int:
+    return _lib().moe_op_sync_status(_stream(stream))
+
+
+def moe_op_set_wait_limit(limit_ns: int) -> None:
+    _check(_lib().moe_op_set_wait_limit(limit_ns), "moe_op_set_wait_limit")
 
 
 # ---------------------------------------------------------------------------

@@ -51,7 +51,10 @@
  * _forward_host; test and timing hooks (moe_layer_get_routing,
  * moe_layer_debug_unpack, moe_layer_sync_status, moe_layer_last_launch_count,
  * moe_layer_set_profiling, moe_layer_kernel_times); moe_route_topk_noalloc;
- * the host-only planner moe_plan_reduce / moe_plan_restore; moe_status_string.
+ * the stand-alone operators moe_block_norm, moe_quantize_rows,
+ * moe_int8_matmul and moe_grouped_matmul (with moe_op_sync_status and
+ * moe_op_set_wait_limit); the host-only planner moe_plan_reduce /
+ * moe_plan_restore; moe_status_string.
  *
  * Conventions.
  *   - Every call returns a moe_status_t; nothing aborts or throws across the ABI.
@@ -308,6 +311,116 @@ int moe_layer_kernel_times(moe_layer_t* layer, const char** names, float* ms, in
  * errors (MOE_ERR_CUDA) and argument errors. */
 moe_status_t moe_route_topk_noalloc(const float* router_logits, int T, int E, int top_k, unsigned flags, int* idx,
                                     float* w, int* counts, int* offsets, void* cuda_stream);
+
+/* ---- Stand-alone operators around the experts ----
+ * What a transformer block does next to the expert layer, on the caller's
+ * tensors: the norms, gate and residual on both sides of a block, and the
+ * products of experts (routed or shared) that are kept at 8 or 16 bits instead
+ * of 2-4. None of them allocates device memory, keeps a workspace or state
+ * between calls, or uses floating-point atomics: calls on different streams do
+ * not interact, every call can be captured into a CUDA graph, and repeated
+ * calls give the same bits. All are asynchronous on cuda_stream, whose device
+ * must be the current one and hold every tensor.
+ * Strides are in elements; a row's elements are contiguous. A call with no
+ * rows returns MOE_OK and launches nothing.
+ * Errors: MOE_ERR_INVALID_ARG (a pointer, size, stride or type),
+ * MOE_ERR_TOO_LARGE (a size limit named below), MOE_ERR_CUDA. The products'
+ * kernels bound every wait between their roles; one that runs out shows at
+ * moe_op_sync_status as MOE_ERR_TIMEOUT, and that call's output is undefined. */
+typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype_t;
+
+/* Norms before and after a block, fused with its gate, the residual scale and
+ * the combination of the experts' rows. Per token t, in fp32 throughout:
+ *   b  = branch[t]                                        (pairs = 0)
+ *      = sum_j pair_weights[t, j] * branch[inv_pos[t, j]] (pairs > 0, in slot
+ *        order; an inv_pos outside [0, branch_rows) adds nothing: a dropped pair)
+ *   n  = b * rsqrt(mean(b^2) + eps) * (weight_offset + post_weight)   (post_weight set, else n = b)
+ *   r' = residual_scale * residual[t] + branch_scale * g * n
+ *   h  = r' * rsqrt(mean(r'^2) + eps) * (weight_offset + pre_weight)  (pre_weight set)
+ * r' enters h unrounded. branch NULL: r' = residual_scale * residual (the plain
+ * norm before a block). residual NULL: r' = branch_scale * g * n. residual_out
+ * and h may each be NULL (not written), not both; h and pre_weight are given
+ * together. gate NULL: g = 1; else g = gate[t * gate_token_stride + c *
+ * gate_channel_stride] with a channel stride of 0 (one value per token) or 1,
+ * through a sigmoid if gate_sigmoid.
+ * residual_out may be residual itself; h may be branch itself when pairs = 0.
+ * No other overlap. width <= 16384, else MOE_ERR_TOO_LARGE. Sums of squares are
+ * fp32: values must stay below about 1e17. */
+typedef struct {
+  int tokens, width;
+  moe_dtype_t dtype;          /* branch, norm weights, gate, h: MOE_BF16 or MOE_FP16 */
+  moe_dtype_t residual_dtype; /* residual, residual_out: dtype or MOE_FP32 */
+  const void* branch;
+  long long branch_stride;
+  int branch_rows;
+  int pairs;                  /* k of the combination, 0..8; 0: branch has one row per token */
+  const int* inv_pos;         /* int32 [tokens, pairs] */
+  const float* pair_weights;  /* fp32 [tokens, pairs] */
+  const void* post_weight;    /* [width] */
+  const void* gate;
+  long long gate_token_stride;
+  int gate_channel_stride;
+  int gate_sigmoid;
+  const void* residual;
+  long long residual_stride;
+  float residual_scale, branch_scale;
+  const void* pre_weight;     /* [width] */
+  float eps, weight_offset;   /* eps >= 0; weight_offset 1 for norms stored as w - 1 */
+  void* residual_out;
+  long long residual_out_stride;
+  void* h;
+  long long h_stride;
+} moe_block_norm_t;
+moe_status_t moe_block_norm(const moe_block_norm_t* args, void* cuda_stream);
+
+/* Activations to 8 bits, one scale per row: with a = max|x[s]|,
+ *   scales[i] = a / 127,  codes[i, c] = round_half_even(127 * x[s, c] / a),
+ * s = src_rows[i] (the gather into expert order, e.g. perm_token) or i when
+ * src_rows is NULL (then rows = x_rows). The codes are the exact roundings of
+ * the quotient. A row of zeros, and a src_rows entry outside [0, x_rows), gives
+ * codes 0 with scale 0; a row that holds a NaN or an infinity gives codes 0
+ * with scale NaN, so that its products are NaN and nothing else's.
+ * x: MOE_BF16 or MOE_FP16 [x_rows, width], width <= 16384 (MOE_ERR_TOO_LARGE);
+ * codes int8 [rows, width]; scales fp32 [rows]. */
+moe_status_t moe_quantize_rows(const void* x, long long x_stride, int x_rows, moe_dtype_t dtype, const int* src_rows,
+                               int rows, int width, signed char* codes, long long codes_stride, float* scales,
+                               void* cuda_stream);
+
+/* Products of 8-bit integers, scaled per row and per output channel, grouped
+ * by expert: for the rows r of expert e, offsets[e] <= r < offsets[e + 1],
+ *   y[r, n] = row_scales[r] * channel_scales[e, n] * sum_k x[r, k] * w[e, n, k]
+ * with exact int32 sums, scaled in fp32 and rounded once to y_dtype.
+ * offsets: int32 [experts + 1] on the device, ascending within [0, rows] (as
+ * moe_route_topk_noalloc writes them), or NULL with experts = 1 (all rows).
+ * An expert may have no rows; rows outside every expert's range are left as
+ * they were. Offsets that descend or leave the range are read as their running
+ * maximum clamped to [0, rows].
+ * x int8 [rows, K], w int8 [experts, N, K], channel_scales fp32 [experts, N],
+ * y [rows, N] of y_dtype. K <= 131071 (int32 sums), experts <= 256, else
+ * MOE_ERR_TOO_LARGE. Pointers and strides of x and w that are not multiples of
+ * 16 bytes, which bulk copies cannot address, take a slower kernel. */
+moe_status_t moe_int8_matmul(const signed char* x, long long x_stride, const float* row_scales, const signed char* w,
+                             long long w_stride, long long expert_stride, const float* channel_scales,
+                             const int* offsets, int rows, int experts, int K, int N, void* y, long long y_stride,
+                             moe_dtype_t y_dtype, void* cuda_stream);
+
+/* The same grouped by expert for 16-bit experts: y[r, n] = sum_k x[r, k] *
+ * w[e, n, k], fp32 sums, rounded once to y_dtype. x and w share dtype (MOE_BF16
+ * or MOE_FP16). offsets, limits (experts) and strides as above. */
+moe_status_t moe_grouped_matmul(const void* x, long long x_stride, const void* w, long long w_stride,
+                                long long expert_stride, const int* offsets, int rows, int experts, int K, int N,
+                                moe_dtype_t dtype, void* y, long long y_stride, moe_dtype_t y_dtype,
+                                void* cuda_stream);
+
+/* Synchronise cuda_stream and return what the products' own device-side checks
+ * found on the current device since the last call (MOE_ERR_TIMEOUT: a bounded
+ * wait gave up), then clear it; MOE_ERR_CUDA for a pending CUDA error. Call it
+ * while no product runs on another stream of the device. */
+moe_status_t moe_op_sync_status(void* cuda_stream);
+
+/* Limit, in nanoseconds, of the products' waits between roles, for the whole
+ * process; 0 restores the default of 2 s. Takes effect at the next call. */
+moe_status_t moe_op_set_wait_limit(unsigned long long limit_ns);
 
 /* ---- Bitwidth planner (host only) ----
  * PagedWeight ("What carries the argument"): under memory pressure the planner
