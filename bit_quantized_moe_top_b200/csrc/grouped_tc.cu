@@ -1,0 +1,608 @@
+// Products grouped by expert on the 5th-generation tensor cores:
+//   y[r, n] = xs[r] ws[e, n] sum_k x[r, k] w[e, n, k]   (8-bit, int32 sums)
+//   y[r, n] = sum_k x[r, k] w[e, n, k]                  (16-bit, fp32 sums)
+//
+// The weights are the MMA's M operand and the rows its N operand, so that a
+// group of any size fills the tensor cores' 128 (or, over a CTA pair, 256)
+// lanes with output channels and only pays for its own rows: N follows the
+// rows of the tile in steps of 16 or 32. Both operands are K-major tiles of
+// 128-byte rows (64 fp16 or 128 int8) brought in by TMA with the 128-byte
+// swizzle, zero-filled past K, N and the last row; rows of a tile that belong
+// to the next group are computed and not stored (columns of D are independent).
+//
+// Two forms of one kernel:
+//   CG = 2  CTA pair, 256 channels x up to 256 rows, persistent over the tiles
+//           of all experts, accumulators double-buffered in TMEM so that the
+//           epilogue of one tile runs under the MMAs of the next;
+//   CG = 1  128 channels x up to 128 rows per CTA for calls with few tiles; a
+//           cluster of S CTAs splits K and adds the partial sums in rank order
+//           through distributed shared memory, each CTA finishing n / S rows.
+// Roles: warp 0 TMA producer, warp 1 MMA (of the pair's first CTA), warps 4-7
+// epilogue. Every mbarrier wait is bounded; one that runs out sets the status
+// word, every role of the CTA stops at its next wait, the cluster drains its
+// copies and MMAs, frees TMEM and returns.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "kernels.h"
+#include "ops.cuh"
+#include "tc.cuh"
+
+namespace moeq {
+
+__device__ unsigned g_op_status;
+
+namespace {
+
+constexpr int kThreadsTc = 256;
+constexpr int kRowBytes = 128;                 // K bytes per stage
+constexpr int kABytes = 128 * kRowBytes;       // 128 channels
+constexpr int kBoxRows = 32;                   // rows per TMA box of x
+constexpr int kBoxBytes = kBoxRows * kRowBytes;
+constexpr int kMaxStagesTc = 10;
+constexpr int kBandTc = 8;                     // row tiles that share a sweep over the channels
+constexpr int kStagingBytes = 2 * 16 * 128 * 4;
+
+struct TcArgs {
+  CUtensorMap map_w;   // [E][N][K], box 128 rows
+  CUtensorMap map_x;   // [rows][K], box 32 rows
+  GroupedArgs g;
+  uint32_t idesc;      // without the N field
+  int NF;              // channel tiles
+  int nmax;            // rows per tile
+  int stages, bslot;   // ring depth, bytes of a stage's x part
+  int S;               // CTAs splitting K (CG = 1)
+  int vec;             // y rows start at 8-byte boundaries
+};
+
+struct RowTilesTc {
+  int nmax;
+  __device__ int operator()(int n) const { return (n + nmax - 1) / nmax; }
+};
+
+// ---- cluster helpers
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_tx_cluster(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+// makes what other CTAs of the cluster wrote before their arrivals visible
+__device__ __forceinline__ void fence_acquire_cluster() { asm volatile("fence.acq_rel.cluster;\n" ::: "memory"); }
+
+// ---- tcgen05 and TMA forms of one CTA or a CTA pair
+template <int CG>
+__device__ __forceinline__ void tma2(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+template <int CG, bool I8>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int acc) {
+  if constexpr (CG == 1 && !I8)
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+  else if constexpr (CG == 1)
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+  else if constexpr (!I8)
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+  else
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// arrives on the barrier at this offset in every CTA of the group once the MMAs issued so far are done
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (CG == 1)
+    mma_commit(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(bar), "h"((uint16_t)3) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void alloc_tmem(uint32_t slot, uint32_t cols) {
+  if constexpr (CG == 1) {
+    tmem_alloc(slot, cols);
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(slot), "r"(cols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void free_tmem(uint32_t addr, uint32_t cols) {
+  if constexpr (CG == 1) tmem_dealloc(addr, cols);
+  else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(addr), "r"(cols));
+}
+// whether ok holds in all n threads of named barrier id
+__device__ __forceinline__ bool named_bar_all(int id, int n, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.cta.red.and.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+struct Tile {
+  int e, r0, live, n, f0;  // expert, first row, rows to store, rows computed, first channel
+};
+// Tile i of the call: experts in order; within one, bands of kBandTc row tiles
+// sweep the channels together, so that the CTAs running at one time read about
+// as many distinct weight rows as activation rows.
+template <int CG>
+__device__ __forceinline__ Tile tile_of(const GroupTable& g, const TcArgs& a, int i) {
+  constexpr int kUnit = 16 * CG;
+  Tile t;
+  t.e = find_group(g, a.g.E, i / a.NF);
+  const int nt = g.first[t.e + 1] - g.first[t.e], rows = g.rows[t.e];
+  const int local = i - g.first[t.e] * a.NF;
+  const int band = local / (kBandTc * a.NF), in = local - band * kBandTc * a.NF;
+  const int bt = min(kBandTc, nt - band * kBandTc);
+  const int f = in / bt, tk = band * kBandTc + in - f * bt;
+  // equal widths: a group's last tile is not much emptier than the others
+  const int width = ((rows + nt - 1) / nt + kUnit - 1) / kUnit * kUnit;
+  t.live = min(width, rows - tk * width);
+  t.n = (t.live + kUnit - 1) / kUnit * kUnit;
+  t.r0 = g.begin[t.e] + tk * width;
+  t.f0 = f * 128 * CG;
+  return t;
+}
+
+template <typename TO>
+__device__ __forceinline__ float scaled(uint32_t v, bool i8, float s) {
+  return i8 ? (float)(int)v * s : __uint_as_float(v);
+}
+
+// 32 (or 16) accumulator columns of this thread's channel to y: 16-bit outputs
+// cross shared memory as pairs of rows so that a warp stores 128 channels of
+// one row at a time, 8 bytes a lane.
+template <typename TO, bool I8>
+__device__ __forceinline__ void store_chunk(const TcArgs& a, const Tile& t, int c0, const uint32_t (&v)[32], float ws,
+                                            const float* xs, uint32_t* stage, int ch0, int tid) {
+  const int warp = tid >> 5, lane = tid & 31;
+  if constexpr (sizeof(TO) == 4) {
+    if (ch0 + tid >= a.g.N) return;
+    float* y = static_cast<float*>(a.g.y) + (long long)(t.r0 + c0) * a.g.ldy + ch0 + tid;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (c0 + j < t.live) y[j * a.g.ldy] = scaled<TO>(v[j], I8, I8 ? ws * xs[c0 + j] : 0.f);
+  } else {
+#pragma unroll
+    for (int p = 0; p < 16; ++p)
+      stage[p * 128 + tid] = pack2<TO>(scaled<TO>(v[2 * p], I8, I8 ? ws * xs[c0 + 2 * p] : 0.f),
+                                       scaled<TO>(v[2 * p + 1], I8, I8 ? ws * xs[c0 + 2 * p + 1] : 0.f));
+    named_bar_sync(1, 128);
+    const int ch = ch0 + 4 * lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = warp * 4 + i;
+      if (c0 + 2 * p >= t.live) continue;
+      const uint4 q = *reinterpret_cast<const uint4*>(stage + p * 128 + 4 * lane);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (c0 + 2 * p + h >= t.live) continue;
+        const uint32_t sel = h ? 0x7632u : 0x5410u;
+        const uint2 o = make_uint2(prmt(q.x, q.y, sel), prmt(q.z, q.w, sel));
+        TO* y = static_cast<TO*>(a.g.y) + (long long)(t.r0 + c0 + 2 * p + h) * a.g.ldy + ch;
+        if (a.vec && ch + 4 <= a.g.N) {
+          *reinterpret_cast<uint2*>(y) = o;
+        } else {
+          const uint32_t w[2] = {o.x, o.y};
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const uint16_t s = (uint16_t)(w[b >> 1] >> (16 * (b & 1)));
+            if (ch + b < a.g.N) reinterpret_cast<uint16_t*>(y)[b] = s;
+          }
+        }
+      }
+    }
+  }
+}
+
+template <int CG, bool I8, typename TO>
+__global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_constant__ TcArgs a) {
+  extern __shared__ uint8_t raw[];
+  __shared__ GroupTable g;
+  __shared__ float xs_s[2][256];
+  __shared__ __align__(8) uint64_t bars_s[2 * kMaxStagesTc + 6];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_s, issued_s;
+  __shared__ uint32_t cluster_abort;
+  constexpr int kUnitCols = CG == 2 ? 256 : 128;  // TMEM columns of one accumulator
+  constexpr uint32_t kCols = 2 * kUnitCols;
+  constexpr int kElem = I8 ? 128 : 64;            // elements per 128-byte row
+  const uint32_t pad = (1024u - (smem_u32(raw) & 1023u)) & 1023u;
+  uint8_t* sm = raw + pad;
+  const uint32_t sbase = smem_u32(sm);
+  const int stage_bytes = kABytes + a.bslot;
+  uint8_t* tail = sm + a.stages * stage_bytes;    // staging (CG = 2) or partial sums (CG = 1)
+  const uint32_t bars = smem_u32(bars_s);
+  auto full = [&](int s) { return bars + 8 * s; };
+  auto empty = [&](int s) { return bars + 8 * (kMaxStagesTc + s); };
+  auto acc_full = [&](int b) { return bars + 8 * (2 * kMaxStagesTc + b); };
+  auto acc_empty = [&](int b) { return bars + 8 * (2 * kMaxStagesTc + 2 + b); };
+  const uint32_t drained = bars + 8 * (2 * kMaxStagesTc + 4), summed = bars + 8 * (2 * kMaxStagesTc + 5);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int csize = CG == 2 ? 2 : a.S;
+  const int cluster = blockIdx.x / csize, nclusters = gridDim.x / csize;
+  const int lead = CG == 2 ? 0 : (int)rank;       // CTA whose MMA warp consumes this CTA's stages
+  volatile int* aborted = &abort_s;
+  unsigned* status = &g_op_status;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(full(s), CG);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), 1);
+      mbar_init(acc_empty(b), 4 * CG);
+    }
+    mbar_init(drained, 1);
+    mbar_init(summed, 4 * (CG == 1 ? a.S : 1));
+    abort_s = 0;
+    cluster_abort = 0;
+    issued_s = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) alloc_tmem<CG>(smem_u32(&tmem_slot), kCols);
+  pdl_wait();
+  pdl_trigger();
+  build_group_table(g, a.g.offsets, a.g.rows, a.g.E, RowTilesTc{a.nmax});
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int total = g.first[a.g.E] * a.NF;
+  const int nk = (a.g.K + kElem - 1) / kElem;
+  const int kb0 = CG == 1 ? nk * (int)rank / a.S : 0, kb1 = CG == 1 ? nk * ((int)rank + 1) / a.S : nk;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int slot = 0, round = 0, issued = 0;
+      bool ok = true;
+      for (int i = cluster; i < total && ok; i += nclusters) {
+        const Tile t = tile_of<CG>(g, a, i);
+        const int nb = (t.n / CG + kBoxRows - 1) / kBoxRows;
+        const uint32_t bytes = kABytes + nb * kBoxBytes;
+        const int row = t.r0 + (CG == 2 ? (int)rank * (t.n / 2) : 0), ch = t.f0 + (CG == 2 ? (int)rank * 128 : 0);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (*aborted || (round > 0 && !mbar_wait_fast(empty(slot), (round - 1) & 1, status, a.g.wait_ns))) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = CG == 2 ? map_rank(full(slot), 0) : full(slot);
+          if constexpr (CG == 2) arrive_tx_cluster(bar, bytes);
+          else mbar_expect_tx(bar, bytes);
+          const uint32_t dst = sbase + slot * stage_bytes;
+          tma3<CG>(dst, &a.map_w, kb * kElem, ch, t.e, bar);
+          for (int b = 0; b < nb; ++b)
+            tma2<CG>(dst + kABytes + b * kBoxBytes, &a.map_x, kb * kElem, row + b * kBoxRows, bar);
+          ++issued;
+          if (++slot == a.stages) {
+            slot = 0;
+            ++round;
+          }
+        }
+      }
+      issued_s = issued;
+      if (!ok) *aborted = 1;
+      // the last arrivals on this CTA's empty barriers land before it may exit
+      for (int u = max(0, issued - a.stages); u < issued && !*aborted; ++u)
+        if (!mbar_wait(empty(u % a.stages), (u / a.stages) & 1, status, kDrainLimitNs)) *aborted = 1;
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && (CG == 1 || rank == 0)) {
+      int slot = 0, ph = 0, it = 0;
+      bool ok = true;
+      for (int i = cluster; i < total && ok; i += nclusters, ++it) {
+        const Tile t = tile_of<CG>(g, a, i);
+        const int buf = it & 1;
+        if (it >= 2 && (*aborted || !mbar_wait_fast(acc_empty(buf), ((it >> 1) - 1) & 1, status, a.g.wait_ns))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t idesc = a.idesc | ((uint32_t)(t.n >> 3) << 17);
+        const uint32_t d = tmem + buf * kUnitCols;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (*aborted || !mbar_wait_fast(full(slot), ph, status, a.g.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = sw128_desc(sbase + slot * stage_bytes), bd = sw128_desc(sbase + slot * stage_bytes + kABytes);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_ss<CG, I8>(d, ad + 2 * k, bd + 2 * k, idesc, kb > kb0 || k > 0);
+          commit<CG>(empty(slot));
+          if (++slot == a.stages) {
+            slot = 0;
+            ph ^= 1;
+          }
+        }
+        if (ok) commit<CG>(acc_full(buf));
+      }
+      if (!ok) *aborted = 1;
+      // every MMA completes before the cluster frees its TMEM
+      if constexpr (CG == 1) mma_commit(drained);
+      else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(drained) : "memory");
+      mbar_wait(drained, 0, status, kDrainLimitNs);
+    }
+  } else if (warp >= 4) {
+    const int tid = threadIdx.x - 128, quarter = warp & 3;
+    int it = 0;
+    for (int i = cluster; i < total; i += nclusters, ++it) {
+      const Tile t = tile_of<CG>(g, a, i);
+      const int buf = it & 1;
+      const int ch0 = t.f0 + (CG == 2 ? (int)rank * 128 : 0);
+      const int ch = ch0 + tid;
+      float ws = 0.f;
+      if constexpr (I8) {
+        for (int j = tid; j < t.n; j += 128) xs_s[buf][j] = j < t.live ? a.g.xs[t.r0 + j] : 0.f;
+        if (ch < a.g.N) ws = a.g.ws[(long long)t.e * a.g.N + ch];
+      }
+      bool ok = !*aborted && mbar_wait_fast(acc_full(buf), (it >> 1) & 1, status, a.g.wait_ns);
+      // the four warps go on together or not at all
+      if (!named_bar_all(2, 128, ok)) {
+        *aborted = 1;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem + buf * kUnitCols + ((uint32_t)(quarter * 32) << 16);
+      if (CG == 2 || a.S == 1) {
+        for (int c0 = 0; c0 < t.n; c0 += 32) {
+          uint32_t v[32];
+          tmem_ld32(d + c0, v);
+          if (c0 + 32 >= t.n) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (CG == 2) arrive_cluster(map_rank(acc_empty(buf), lead));
+              else mbar_arrive(acc_empty(buf));
+            }
+          }
+          store_chunk<TO, I8>(a, t, c0, v, ws, xs_s[buf], reinterpret_cast<uint32_t*>(tail) + ((c0 >> 5) & 1) * 2048, ch0,
+                              tid);
+        }
+      } else {
+        // partial sums of columns [q c, q c + c) go to CTA q, slot [rank]
+        const int c = t.n / a.S;
+        const uint32_t part = smem_u32(tail) + (uint32_t)(((int)rank * c) * 128 + tid) * 4;
+        for (int c0 = 0; c0 < t.n; c0 += 16) {
+          uint32_t v[16];
+          tmem_ld16(d + c0, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int q = (c0 + j) / c;
+            st_cluster_u32(map_rank(part + (uint32_t)(c0 + j - q * c) * 512, q), v[j]);
+          }
+        }
+        __syncwarp();
+        if (lane < a.S) arrive_cluster(map_rank(summed, lane));
+        ok = mbar_wait(summed, 0, status, a.g.wait_ns);
+        fence_acquire_cluster();
+        if (!ok) {
+          *aborted = 1;
+          break;
+        }
+        const uint32_t* sums = reinterpret_cast<const uint32_t*>(tail) + tid;
+        for (int j = 0; j < c; ++j) {
+          const int col = (int)rank * c + j;
+          if (col >= t.live || ch >= a.g.N) break;
+          float y;
+          if constexpr (I8) {
+            int s = 0;
+            for (int q = 0; q < a.S; ++q) s += (int)sums[(q * c + j) * 128];
+            y = (float)s * (ws * xs_s[buf][col]);
+          } else {
+            float s = 0.f;
+            for (int q = 0; q < a.S; ++q) s += __uint_as_float(sums[(q * c + j) * 128]);
+            y = s;
+          }
+          static_cast<TO*>(a.g.y)[(long long)(t.r0 + col) * a.g.ldy + ch] = from_f32<TO>(y);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && abort_s)
+    for (int q = 0; q < csize; ++q) st_cluster_u32(map_rank(smem_u32(&cluster_abort), q), 1u);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (*(volatile uint32_t*)&cluster_abort) {
+    // Wait for every copy in flight. A stage that only one CTA of a pair
+    // filled gets the other's arrival here, so that its phase can complete.
+    if (threadIdx.x == 0 && (CG == 1 || rank == 0)) {
+      const int mine = issued_s, other = CG == 2 ? (int)ld_cluster_u32(map_rank(smem_u32(&issued_s), 1)) : mine;
+      const int last = max(mine, other);
+      for (int u = max(0, last - a.stages); u < last; ++u) {
+        if (u >= mine || u >= other) mbar_arrive(full(u % a.stages));
+        mbar_wait(full(u % a.stages), (u / a.stages) & 1, status, kDrainLimitNs);
+      }
+    }
+    cluster_sync();
+  }
+  if (warp == 1) free_tmem<CG>(tmem, kCols);
+  cluster_sync();
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+bool encode_rows(CUtensorMap* m, const void* base, int op, int es, long long K, long long rows, long long ld,
+                 long long E, long long lde, int box_rows) {
+  const CUtensorMapDataType type = op == kOpInt8   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : op == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)rows, (cuuint64_t)E};
+  const cuuint64_t strides[2] = {(cuuint64_t)(ld * es), (cuuint64_t)(lde * es)};
+  const cuuint32_t box[3] = {(cuuint32_t)(kRowBytes / es), (cuuint32_t)box_rows, 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return encode_fn()(m, type, E ? 3 : 2, const_cast<void*>(base), dims, strides, box, one,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kSmemBudget = 221 * 1024;  // dynamic; the static tables take about 6 KiB more
+
+template <int CG, bool I8, typename TO>
+cudaError_t launch_tc(const TcArgs& a, int clusters, size_t smem, cudaStream_t st) {
+  static std::atomic<unsigned long long> set{0};  // devices whose attribute is set
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev > 63 || !(set.load(std::memory_order_acquire) >> dev & 1)) {
+    err = cudaFuncSetAttribute(grouped_tc_kernel<CG, I8, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget);
+    if (err != cudaSuccess) return err;
+    if (dev <= 63) set.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  const int csize = CG == 2 ? 2 : a.S;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(clusters * csize);
+  cfg.blockDim = dim3(kThreadsTc);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = csize;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, I8, TO>, a);
+}
+template <int CG>
+cudaError_t launch_tc_typed(const TcArgs& a, int op, int y_dtype, int clusters, size_t smem, cudaStream_t st) {
+  if (op == kOpInt8) {
+    if (y_dtype == DT_BF16) return launch_tc<CG, true, __nv_bfloat16>(a, clusters, smem, st);
+    if (y_dtype == DT_FP16) return launch_tc<CG, true, __half>(a, clusters, smem, st);
+    return launch_tc<CG, true, float>(a, clusters, smem, st);
+  }
+  if (y_dtype == DT_BF16) return launch_tc<CG, false, __nv_bfloat16>(a, clusters, smem, st);
+  if (y_dtype == DT_FP16) return launch_tc<CG, false, __half>(a, clusters, smem, st);
+  return launch_tc<CG, false, float>(a, clusters, smem, st);
+}
+
+}  // namespace
+
+// Whether TMA can address the operands: 16-byte bases and strides, rows that do
+// not overlap, tile counts within an int.
+bool grouped_tc_fits(const GroupedArgs& a, int op) {
+  const long long es = op == kOpInt8 ? 1 : 2;
+  auto m16 = [](long long v) { return v % 16 == 0; };
+  const long long lim = 1LL << 39;
+  if (!encode_fn()) return false;
+  if (!m16((long long)reinterpret_cast<uintptr_t>(a.x)) || !m16((long long)reinterpret_cast<uintptr_t>(a.w))) return false;
+  if ((a.rows > 1 && (!m16(a.ldx * es) || a.ldx < a.K)) || !m16(a.ldw * es) || a.ldw < a.K) return false;
+  if (a.E > 1 && (!m16(a.ldwe * es) || a.ldwe % a.ldw || a.ldwe < (a.N - 1) * a.ldw + a.K)) return false;
+  if (a.ldx * es >= lim || a.ldw * es * a.N >= lim || a.ldwe * es >= lim) return false;
+  return ((long long)a.rows / 16 + a.E) * (a.N / 128 + 1) < (1LL << 30);
+}
+
+cudaError_t launch_grouped_tc(const GroupedArgs& g, int op, int y_dtype, cudaStream_t st) {
+  const int es = op == kOpInt8 ? 1 : 2;
+  const int sms = device_sms(), pairs = sms / 2;
+  TcArgs a{};
+  a.g = g;
+  const long long ldx = g.rows > 1 ? g.ldx : (g.K + 15) / 16 * 16;
+  const long long ldwe = g.E > 1 ? g.ldwe : g.ldw * g.N;
+  if (!encode_rows(&a.map_w, g.w, op, es, g.K, g.N, g.ldw, g.E, ldwe, 128) ||
+      !encode_rows(&a.map_x, g.x, op, es, g.K, g.rows, ldx, 0, 0, kBoxRows))
+    return cudaErrorInvalidValue;
+  a.vec = reinterpret_cast<uintptr_t>(g.y) % 8 == 0 && g.ldy % 4 == 0;
+  a.idesc = op == kOpInt8 ? (2u << 4) | (1u << 7) | (1u << 10)
+                          : (1u << 4) | ((op == DT_BF16 ? 1u : 0u) << 7) | ((op == DT_BF16 ? 1u : 0u) << 10);
+  const int nk = (g.K * es + kRowBytes - 1) / kRowBytes;
+  // row tiles: at most one partial tile per group that can have rows
+  const long long groups = std::min<long long>(g.rows, g.E);
+  const long long wide = (groups + g.rows / 256) * ((g.N + 255) / 256);
+  if (wide > pairs || g.rows > 128 * g.E) {
+    a.idesc |= (uint32_t)(256 >> 4) << 24;
+    a.NF = (g.N + 255) / 256;
+    a.nmax = 256;
+    a.S = 1;
+    a.bslot = 128 * kRowBytes;
+    a.stages = 6;
+    const size_t smem = (size_t)a.stages * (kABytes + a.bslot) + kStagingBytes + 1024;
+    return launch_tc_typed<2>(a, op, y_dtype, (int)std::min<long long>(wide, pairs), smem, st);
+  }
+  a.idesc |= (uint32_t)(128 >> 4) << 24;
+  a.NF = (g.N + 127) / 128;
+  a.nmax = std::min(128, (g.rows + 15) / 16 * 16);
+  const long long tiles = (groups + g.rows / a.nmax) * a.NF;
+  a.S = 1;
+  while (a.S < 8 && tiles * a.S * 2 <= sms && nk >= a.S * 4) a.S *= 2;
+  a.bslot = (a.nmax + kBoxRows - 1) / kBoxRows * kBoxBytes;
+  const int fixed = (a.S > 1 ? a.nmax * 512 : kStagingBytes) + 1024;
+  a.stages = std::min({kMaxStagesTc, (kSmemBudget - fixed) / (kABytes + a.bslot), std::max(2, (nk + a.S - 1) / a.S)});
+  const size_t smem = (size_t)a.stages * (kABytes + a.bslot) + fixed;
+  const int clusters = (int)(a.S > 1 ? tiles : std::min<long long>(tiles, sms));
+  return launch_tc_typed<1>(a, op, y_dtype, clusters, smem, st);
+}
+
+cudaError_t read_op_status(unsigned* out, cudaStream_t st) {
+  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_op_status, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  const unsigned zero = 0;
+  if (e == cudaSuccess && *out) e = cudaMemcpyToSymbolAsync(g_op_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  return e;
+}
+
+}  // namespace moeq

@@ -30,7 +30,8 @@ moe_status_t check_product(const void* x, long long ldx, const void* w, long lon
 
 moe_status_t run_product(GroupedArgs& a, int op, int y_dtype, cudaStream_t st) {
   a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
-  return cuda_status(launch_grouped_plain(a, op, y_dtype, st));
+  return cuda_status(grouped_tc_fits(a, op) ? launch_grouped_tc(a, op, y_dtype, st)
+                                            : launch_grouped_plain(a, op, y_dtype, st));
 }
 
 }  // namespace
@@ -128,7 +129,9 @@ moe_status_t moe_grouped_matmul(const void* x, long long x_stride, const void* w
 }
 
 moe_status_t moe_op_sync_status(void* cuda_stream) {
-  return cuda_status(cudaStreamSynchronize(static_cast<cudaStream_t>(cuda_stream)));
+  unsigned s = 0;
+  if (read_op_status(&s, static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) return MOE_ERR_CUDA;
+  return s & ST_TIMEOUT ? MOE_ERR_TIMEOUT : s ? MOE_ERR_DEVICE_CHECK : MOE_OK;
 }
 
 moe_status_t moe_op_set_wait_limit(unsigned long long limit_ns) {
