@@ -17,7 +17,7 @@
 //   CG = 1  128 channels x up to 128 rows per CTA for calls with few tiles; a
 //           cluster of S CTAs splits K and adds the partial sums in rank order
 //           through distributed shared memory, each CTA finishing n / S rows.
-// Roles: warp 0 TMA producer, warp 1 MMA (of the pair's first CTA), warps 4-7
+// Roles: warp 0 TMA producer, warp 1 MMA (of the pair's first CTA), warps 2-9
 // epilogue. Every mbarrier wait is bounded; one that runs out sets the status
 // word, every role of the CTA stops at its next wait, the cluster drains its
 // copies and MMAs, frees TMEM and returns.
@@ -36,18 +36,19 @@ __device__ unsigned g_op_status;
 
 namespace {
 
-constexpr int kThreadsTc = 256;
+constexpr int kEpiWarps = 8;
+constexpr int kThreadsTc = 64 + 32 * kEpiWarps;
 constexpr int kRowBytes = 128;                 // K bytes per stage
 constexpr int kABytes = 128 * kRowBytes;       // 128 channels
-constexpr int kBoxRows = 32;                   // rows per TMA box of x
+constexpr int kBoxRows = 32;                   // unit of the rows per TMA box of x
 constexpr int kBoxBytes = kBoxRows * kRowBytes;
 constexpr int kMaxStagesTc = 10;
 constexpr int kBandTc = 8;                     // row tiles that share a sweep over the channels
-constexpr int kStagingBytes = 2 * 16 * 128 * 4;
+constexpr int kStagingBytes = kEpiWarps * 2048;
 
 struct TcArgs {
   CUtensorMap map_w;   // [E][N][K], box 128 rows
-  CUtensorMap map_x;   // [rows][K], box 32 rows
+  CUtensorMap map_x[4];  // [rows][K], boxes of 32, 64, 96 and 128 rows: one copy per stage
   GroupedArgs g;
   uint32_t idesc;      // without the N field
   int NF;              // channel tiles
@@ -153,17 +154,6 @@ __device__ __forceinline__ void free_tmem(uint32_t addr, uint32_t cols) {
   if constexpr (CG == 1) tmem_dealloc(addr, cols);
   else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(addr), "r"(cols));
 }
-// whether ok holds in all n threads of named barrier id
-__device__ __forceinline__ bool named_bar_all(int id, int n, bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.cta.red.and.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(id), "r"(n), "r"(ok ? 1u : 0u)
-      : "memory");
-  return r != 0;
-}
-
 struct Tile {
   int e, r0, live, n, f0;  // expert, first row, rows to store, rows computed, first channel
 };
@@ -180,60 +170,105 @@ __device__ __forceinline__ Tile tile_of(const GroupTable& g, const TcArgs& a, in
   const int band = local / (kBandTc * a.NF), in = local - band * kBandTc * a.NF;
   const int bt = min(kBandTc, nt - band * kBandTc);
   const int f = in / bt, tk = band * kBandTc + in - f * bt;
-  // equal widths: a group's last tile is not much emptier than the others
-  const int width = ((rows + nt - 1) / nt + kUnit - 1) / kUnit * kUnit;
-  t.live = min(width, rows - tk * width);
-  t.n = (t.live + kUnit - 1) / kUnit * kUnit;
-  t.r0 = g.begin[t.e] + tk * width;
+  // widths in MMA units that differ by one at most, so that no tile reads its
+  // weights for a few rows only
+  const int units = (rows + kUnit - 1) / kUnit, base = units / nt, more = units - base * nt;
+  const int u0 = tk * base + min(tk, more);
+  t.n = (base + (tk < more ? 1 : 0)) * kUnit;
+  t.live = min(t.n, rows - u0 * kUnit);
+  t.r0 = g.begin[t.e] + u0 * kUnit;
   t.f0 = f * 128 * CG;
   return t;
 }
 
-template <typename TO>
-__device__ __forceinline__ float scaled(uint32_t v, bool i8, float s) {
-  return i8 ? (float)(int)v * s : __uint_as_float(v);
+template <bool I8>
+__device__ __forceinline__ float scaled(uint32_t v, float s) {
+  if constexpr (I8) return (float)(int)v * s;
+  else return __uint_as_float(v);
 }
 
-// 32 (or 16) accumulator columns of this thread's channel to y: 16-bit outputs
-// cross shared memory as pairs of rows so that a warp stores 128 channels of
-// one row at a time, 8 bytes a lane.
+// 32 columns (rows of y from row c0 of the tile) of the accumulator into registers
+__device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// The loaded registers may be read only after this (they pass through it, so
+// that no use moves ahead of the wait).
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// One warp's 32 channels (lane = channel) of 32 rows to y. 16-bit outputs
+// cross the warp's 2 KiB of shared memory as pairs of rows, so that a store
+// covers four rows of 32 channels, 8 bytes a lane; 32-bit outputs go out
+// directly, one row of 32 channels per store.
 template <typename TO, bool I8>
 __device__ __forceinline__ void store_chunk(const TcArgs& a, const Tile& t, int c0, const uint32_t (&v)[32], float ws,
-                                            const float* xs, uint32_t* stage, int ch0, int tid) {
-  const int warp = tid >> 5, lane = tid & 31;
-  if constexpr (sizeof(TO) == 4) {
-    if (ch0 + tid >= a.g.N) return;
-    float* y = static_cast<float*>(a.g.y) + (long long)(t.r0 + c0) * a.g.ldy + ch0 + tid;
+                                            uint32_t* stage, float* xs, int ch0, int lane) {
+  float sc[32];
+  if constexpr (I8) {
+    xs[lane] = c0 + lane < t.live ? a.g.xs[t.r0 + c0 + lane] : 0.f;
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (c0 + j < t.live) y[j * a.g.ldy] = scaled<TO>(v[j], I8, I8 ? ws * xs[c0 + j] : 0.f);
+    for (int j = 0; j < 32; j += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(xs + j);
+      sc[j] = ws * x.x;
+      sc[j + 1] = ws * x.y;
+      sc[j + 2] = ws * x.z;
+      sc[j + 3] = ws * x.w;
+    }
+  }
+  const int rows = t.live - c0;  // rows to store, maybe more than 32
+  if constexpr (sizeof(TO) == 4) {
+    if (ch0 + lane < a.g.N) {
+      float* y = static_cast<float*>(a.g.y) + (long long)(t.r0 + c0) * a.g.ldy + ch0 + lane;
+      if (rows >= 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) y[j * a.g.ldy] = scaled<I8>(v[j], I8 ? sc[j] : 0.f);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j < rows) y[j * a.g.ldy] = scaled<I8>(v[j], I8 ? sc[j] : 0.f);
+      }
+    }
+    __syncwarp();
   } else {
 #pragma unroll
     for (int p = 0; p < 16; ++p)
-      stage[p * 128 + tid] = pack2<TO>(scaled<TO>(v[2 * p], I8, I8 ? ws * xs[c0 + 2 * p] : 0.f),
-                                       scaled<TO>(v[2 * p + 1], I8, I8 ? ws * xs[c0 + 2 * p + 1] : 0.f));
-    named_bar_sync(1, 128);
-    const int ch = ch0 + 4 * lane;
+      stage[p * 32 + lane] = pack2<TO>(scaled<I8>(v[2 * p], I8 ? sc[2 * p] : 0.f),
+                                       scaled<I8>(v[2 * p + 1], I8 ? sc[2 * p + 1] : 0.f));
+    __syncwarp();
+    uint4 q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int p = warp * 4 + i;
-      if (c0 + 2 * p >= t.live) continue;
-      const uint4 q = *reinterpret_cast<const uint4*>(stage + p * 128 + 4 * lane);
+    for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const uint4*>(stage + (4 * i + (lane >> 3)) * 32 + 4 * (lane & 7));
+    __syncwarp();
+    const int ch = ch0 + 4 * (lane & 7), p0 = lane >> 3;
+    TO* y = static_cast<TO*>(a.g.y) + (long long)(t.r0 + c0 + 2 * p0) * a.g.ldy + ch;
+    if (a.vec && rows >= 32 && ch0 + 32 <= a.g.N) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (c0 + 2 * p + h >= t.live) continue;
-        const uint32_t sel = h ? 0x7632u : 0x5410u;
-        const uint2 o = make_uint2(prmt(q.x, q.y, sel), prmt(q.z, q.w, sel));
-        TO* y = static_cast<TO*>(a.g.y) + (long long)(t.r0 + c0 + 2 * p + h) * a.g.ldy + ch;
-        if (a.vec && ch + 4 <= a.g.N) {
-          *reinterpret_cast<uint2*>(y) = o;
-        } else {
-          const uint32_t w[2] = {o.x, o.y};
+      for (int i = 0; i < 4; ++i) {
+        *reinterpret_cast<uint2*>(y + 8 * i * a.g.ldy) = make_uint2(prmt(q[i].x, q[i].y, 0x5410u), prmt(q[i].z, q[i].w, 0x5410u));
+        *reinterpret_cast<uint2*>(y + (8 * i + 1) * a.g.ldy) = make_uint2(prmt(q[i].x, q[i].y, 0x7632u), prmt(q[i].z, q[i].w, 0x7632u));
+      }
+    } else {
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const uint16_t s = (uint16_t)(w[b >> 1] >> (16 * (b & 1)));
-            if (ch + b < a.g.N) reinterpret_cast<uint16_t*>(y)[b] = s;
-          }
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (8 * i + 2 * p0 + h >= rows) continue;
+          uint16_t* o = reinterpret_cast<uint16_t*>(y + (8 * i + h) * a.g.ldy);
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (ch + b < a.g.N) o[b] = (uint16_t)(w[b] >> (16 * h));
         }
       }
     }
@@ -244,7 +279,7 @@ template <int CG, bool I8, typename TO>
 __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_constant__ TcArgs a) {
   extern __shared__ uint8_t raw[];
   __shared__ GroupTable g;
-  __shared__ float xs_s[2][256];
+  __shared__ __align__(16) float xs_s[kEpiWarps][32];
   __shared__ __align__(8) uint64_t bars_s[2 * kMaxStagesTc + 6];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s, issued_s;
@@ -278,10 +313,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), 4 * CG);
+      mbar_init(acc_empty(b), kEpiWarps * CG);
     }
     mbar_init(drained, 1);
-    mbar_init(summed, 4 * (CG == 1 ? a.S : 1));
+    mbar_init(summed, kEpiWarps * (CG == 1 ? a.S : 1));
     abort_s = 0;
     cluster_abort = 0;
     issued_s = 0;
@@ -307,6 +342,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
         const Tile t = tile_of<CG>(g, a, i);
         const int nb = (t.n / CG + kBoxRows - 1) / kBoxRows;
         const uint32_t bytes = kABytes + nb * kBoxBytes;
+        const CUtensorMap* map_x = &a.map_x[nb - 1];
         const int row = t.r0 + (CG == 2 ? (int)rank * (t.n / 2) : 0), ch = t.f0 + (CG == 2 ? (int)rank * 128 : 0);
         for (int kb = kb0; kb < kb1; ++kb) {
           if (*aborted || (round > 0 && !mbar_wait_fast(empty(slot), (round - 1) & 1, status, a.g.wait_ns))) {
@@ -318,8 +354,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
           else mbar_expect_tx(bar, bytes);
           const uint32_t dst = sbase + slot * stage_bytes;
           tma3<CG>(dst, &a.map_w, kb * kElem, ch, t.e, bar);
-          for (int b = 0; b < nb; ++b)
-            tma2<CG>(dst + kABytes + b * kBoxBytes, &a.map_x, kb * kElem, row + b * kBoxRows, bar);
+          tma2<CG>(dst + kABytes, map_x, kb * kElem, row, bar);
           ++issued;
           if (++slot == a.stages) {
             slot = 0;
@@ -371,47 +406,53 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(drained) : "memory");
       mbar_wait(drained, 0, status, kDrainLimitNs);
     }
-  } else if (warp >= 4) {
-    const int tid = threadIdx.x - 128, quarter = warp & 3;
+  } else {
+    // two warps per 32 channels, taking the tile's column chunks in turn
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    uint32_t* stage = reinterpret_cast<uint32_t*>(tail) + (warp - 2) * 512;
+    float* xs = xs_s[warp - 2];
     int it = 0;
     for (int i = cluster; i < total; i += nclusters, ++it) {
       const Tile t = tile_of<CG>(g, a, i);
       const int buf = it & 1;
-      const int ch0 = t.f0 + (CG == 2 ? (int)rank * 128 : 0);
-      const int ch = ch0 + tid;
+      const int ch0 = t.f0 + (CG == 2 ? (int)rank * 128 : 0) + quarter * 32, ch = ch0 + lane;
       float ws = 0.f;
-      if constexpr (I8) {
-        for (int j = tid; j < t.n; j += 128) xs_s[buf][j] = j < t.live ? a.g.xs[t.r0 + j] : 0.f;
+      if constexpr (I8)
         if (ch < a.g.N) ws = a.g.ws[(long long)t.e * a.g.N + ch];
-      }
       bool ok = !*aborted && mbar_wait_fast(acc_full(buf), (it >> 1) & 1, status, a.g.wait_ns);
-      // the four warps go on together or not at all
-      if (!named_bar_all(2, 128, ok)) {
+      if (!__all_sync(0xffffffffu, ok)) {
         *aborted = 1;
         break;
       }
       tc_fence_after();
       const uint32_t d = tmem + buf * kUnitCols + ((uint32_t)(quarter * 32) << 16);
       if (CG == 2 || a.S == 1) {
-        for (int c0 = 0; c0 < t.n; c0 += 32) {
-          uint32_t v[32];
-          tmem_ld32(d + c0, v);
-          if (c0 + 32 >= t.n) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if constexpr (CG == 2) arrive_cluster(map_rank(acc_empty(buf), lead));
-              else mbar_arrive(acc_empty(buf));
-            }
+        // the next chunk's load is in flight while a chunk is stored
+        uint32_t v[2][32];
+        const int c_first = half * 32;
+        if (c_first < t.n) tmem_ld32_nw(d + c_first, v[0]);
+#pragma unroll 1
+        for (int c0 = c_first; c0 < t.n; c0 += 128) {
+          tmem_wait_ld(v[0]);
+          if (c0 + 64 < t.n) tmem_ld32_nw(d + c0 + 64, v[1]);
+          store_chunk<TO, I8>(a, t, c0, v[0], ws, stage, xs, ch0, lane);
+          if (c0 + 64 < t.n) {
+            tmem_wait_ld(v[1]);
+            if (c0 + 128 < t.n) tmem_ld32_nw(d + c0 + 128, v[0]);
+            store_chunk<TO, I8>(a, t, c0 + 64, v[1], ws, stage, xs, ch0, lane);
           }
-          store_chunk<TO, I8>(a, t, c0, v, ws, xs_s[buf], reinterpret_cast<uint32_t*>(tail) + ((c0 >> 5) & 1) * 2048, ch0,
-                              tid);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2) arrive_cluster(map_rank(acc_empty(buf), lead));
+          else mbar_arrive(acc_empty(buf));
         }
       } else {
         // partial sums of columns [q c, q c + c) go to CTA q, slot [rank]
         const int c = t.n / a.S;
-        const uint32_t part = smem_u32(tail) + (uint32_t)(((int)rank * c) * 128 + tid) * 4;
-        for (int c0 = 0; c0 < t.n; c0 += 16) {
+        const uint32_t part = smem_u32(tail) + (uint32_t)(((int)rank * c) * 128 + quarter * 32 + lane) * 4;
+        for (int c0 = half * 16; c0 < t.n; c0 += 32) {
           uint32_t v[16];
           tmem_ld16(d + c0, v);
 #pragma unroll
@@ -428,15 +469,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
           *aborted = 1;
           break;
         }
-        const uint32_t* sums = reinterpret_cast<const uint32_t*>(tail) + tid;
-        for (int j = 0; j < c; ++j) {
+        const uint32_t* sums = reinterpret_cast<const uint32_t*>(tail) + quarter * 32 + lane;
+        for (int j = half; j < c; j += 2) {
           const int col = (int)rank * c + j;
           if (col >= t.live || ch >= a.g.N) break;
           float y;
           if constexpr (I8) {
             int s = 0;
             for (int q = 0; q < a.S; ++q) s += (int)sums[(q * c + j) * 128];
-            y = (float)s * (ws * xs_s[buf][col]);
+            y = (float)s * (ws * a.g.xs[t.r0 + col]);
           } else {
             float s = 0.f;
             for (int q = 0; q < a.S; ++q) s += __uint_as_float(sums[(q * c + j) * 128]);
@@ -564,9 +605,9 @@ cudaError_t launch_grouped_tc(const GroupedArgs& g, int op, int y_dtype, cudaStr
   a.g = g;
   const long long ldx = g.rows > 1 ? g.ldx : (g.K + 15) / 16 * 16;
   const long long ldwe = g.E > 1 ? g.ldwe : g.ldw * g.N;
-  if (!encode_rows(&a.map_w, g.w, op, es, g.K, g.N, g.ldw, g.E, ldwe, 128) ||
-      !encode_rows(&a.map_x, g.x, op, es, g.K, g.rows, ldx, 0, 0, kBoxRows))
-    return cudaErrorInvalidValue;
+  if (!encode_rows(&a.map_w, g.w, op, es, g.K, g.N, g.ldw, g.E, ldwe, 128)) return cudaErrorInvalidValue;
+  for (int b = 0; b < 4; ++b)
+    if (!encode_rows(&a.map_x[b], g.x, op, es, g.K, g.rows, ldx, 0, 0, (b + 1) * kBoxRows)) return cudaErrorInvalidValue;
   a.vec = reinterpret_cast<uintptr_t>(g.y) % 8 == 0 && g.ldy % 4 == 0;
   a.idesc = op == kOpInt8 ? (2u << 4) | (1u << 7) | (1u << 10)
                           : (1u << 4) | ((op == DT_BF16 ? 1u : 0u) << 7) | ((op == DT_BF16 ? 1u : 0u) << 10);
