@@ -81,11 +81,9 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-// Relaxed: it publishes nothing but the byte count (a release at cluster scope
-// in the producer's loop took about 1 us per stage).
-__device__ __forceinline__ void arrive_tx_cluster(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes)
-               : "memory");
+// takes the place of copies that were announced and never issued
+__device__ __forceinline__ void complete_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
@@ -154,6 +152,14 @@ __device__ __forceinline__ void free_tmem(uint32_t addr, uint32_t cols) {
   if constexpr (CG == 1) tmem_dealloc(addr, cols);
   else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(addr), "r"(cols));
 }
+// Wait of a role: the phase has usually completed; the shared abort flag is
+// looked at only when it has not.
+__device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity, unsigned* status, unsigned long long limit_ns,
+                                          volatile int* aborted) {
+  if (limit_ns >= kSleepLimitNs && mbar_test(bar, parity)) return true;
+  return !*aborted && mbar_wait_slow(bar, parity, status, limit_ns);
+}
+
 struct Tile {
   int e, r0, live, n, f0;  // expert, first row, rows to store, rows computed, first channel
 };
@@ -283,6 +289,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
   __shared__ __align__(8) uint64_t bars_s[2 * kMaxStagesTc + 6];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s, issued_s;
+  __shared__ uint32_t bytes_s[kMaxStagesTc];  // of the stage's last copies
   __shared__ uint32_t cluster_abort;
   constexpr int kUnitCols = CG == 2 ? 256 : 128;  // TMEM columns of one accumulator
   constexpr uint32_t kCols = 2 * kUnitCols;
@@ -308,7 +315,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(full(s), CG);
+      mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -336,6 +343,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
 
   if (warp == 0) {
     if (lane == 0) {
+      // the pair's copies all count on the first CTA's barrier, which that CTA alone announces them to
+      const uint32_t full0 = CG == 2 ? map_rank(full(0), 0) : full(0);
+      const bool announce = CG == 1 || rank == 0;
       int slot = 0, round = 0, issued = 0;
       bool ok = true;
       for (int i = cluster; i < total && ok; i += nclusters) {
@@ -345,16 +355,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
         const CUtensorMap* map_x = &a.map_x[nb - 1];
         const int row = t.r0 + (CG == 2 ? (int)rank * (t.n / 2) : 0), ch = t.f0 + (CG == 2 ? (int)rank * 128 : 0);
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (*aborted || (round > 0 && !mbar_wait_fast(empty(slot), (round - 1) & 1, status, a.g.wait_ns))) {
+          if (round > 0 && !role_wait(empty(slot), (round - 1) & 1, status, a.g.wait_ns, aborted)) {
             ok = false;
             break;
           }
-          const uint32_t bar = CG == 2 ? map_rank(full(slot), 0) : full(slot);
-          if constexpr (CG == 2) arrive_tx_cluster(bar, bytes);
-          else mbar_expect_tx(bar, bytes);
+          if (announce) mbar_expect_tx(full(slot), CG * bytes);
+          bytes_s[slot] = bytes;
           const uint32_t dst = sbase + slot * stage_bytes;
-          tma3<CG>(dst, &a.map_w, kb * kElem, ch, t.e, bar);
-          tma2<CG>(dst + kABytes, map_x, kb * kElem, row, bar);
+          tma3<CG>(dst, &a.map_w, kb * kElem, ch, t.e, full0 + 8 * slot);
+          tma2<CG>(dst + kABytes, map_x, kb * kElem, row, full0 + 8 * slot);
           ++issued;
           if (++slot == a.stages) {
             slot = 0;
@@ -375,7 +384,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
       for (int i = cluster; i < total && ok; i += nclusters, ++it) {
         const Tile t = tile_of<CG>(g, a, i);
         const int buf = it & 1;
-        if (it >= 2 && (*aborted || !mbar_wait_fast(acc_empty(buf), ((it >> 1) - 1) & 1, status, a.g.wait_ns))) {
+        if (it >= 2 && !role_wait(acc_empty(buf), ((it >> 1) - 1) & 1, status, a.g.wait_ns, aborted)) {
           ok = false;
           break;
         }
@@ -383,7 +392,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
         const uint32_t idesc = a.idesc | ((uint32_t)(t.n >> 3) << 17);
         const uint32_t d = tmem + buf * kUnitCols;
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (*aborted || !mbar_wait_fast(full(slot), ph, status, a.g.wait_ns)) {
+          if (!role_wait(full(slot), ph, status, a.g.wait_ns, aborted)) {
             ok = false;
             break;
           }
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
       float ws = 0.f;
       if constexpr (I8)
         if (ch < a.g.N) ws = a.g.ws[(long long)t.e * a.g.N + ch];
-      bool ok = !*aborted && mbar_wait_fast(acc_full(buf), (it >> 1) & 1, status, a.g.wait_ns);
+      bool ok = role_wait(acc_full(buf), (it >> 1) & 1, status, a.g.wait_ns, aborted);
       if (!__all_sync(0xffffffffu, ok)) {
         *aborted = 1;
         break;
@@ -495,14 +504,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
   cluster_sync();
   tc_fence_after();
   if (*(volatile uint32_t*)&cluster_abort) {
-    // Wait for every copy in flight. A stage that only one CTA of a pair
-    // filled gets the other's arrival here, so that its phase can complete.
+    // Wait for every copy in flight. Where one CTA of a pair filled a stage and
+    // the other did not, the missing half is made up here, so that the phase
+    // can complete.
     if (threadIdx.x == 0 && (CG == 1 || rank == 0)) {
       const int mine = issued_s, other = CG == 2 ? (int)ld_cluster_u32(map_rank(smem_u32(&issued_s), 1)) : mine;
       const int last = max(mine, other);
       for (int u = max(0, last - a.stages); u < last; ++u) {
-        if (u >= mine || u >= other) mbar_arrive(full(u % a.stages));
-        mbar_wait(full(u % a.stages), (u / a.stages) & 1, status, kDrainLimitNs);
+        const int s = u % a.stages;
+        if (u >= other) complete_tx(full(s), bytes_s[s]);
+        if (u >= mine) mbar_expect_tx(full(s), ld_cluster_u32(map_rank(smem_u32(&bytes_s[s]), 1)));
+        mbar_wait(full(s), (u / a.stages) & 1, status, kDrainLimitNs);
       }
     }
     cluster_sync();
