@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
   auto acc_full = [&](int b) { return bars + 8 * (2 * kMaxStagesTc + b); };
   auto acc_empty = [&](int b) { return bars + 8 * (2 * kMaxStagesTc + 2 + b); };
   const uint32_t drained = bars + 8 * (2 * kMaxStagesTc + 4), summed = bars + 8 * (2 * kMaxStagesTc + 5);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int csize = CG == 2 ? 2 : a.S;
   const int cluster = blockIdx.x / csize, nclusters = gridDim.x / csize;
@@ -341,78 +341,84 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
   const int nk = (a.g.K + kElem - 1) / kElem;
   const int kb0 = CG == 1 ? nk * (int)rank / a.S : 0, kb1 = CG == 1 ? nk * ((int)rank + 1) / a.S : nk;
 
+  // The copy and MMA warps run their loops whole, with warp-uniform values; one
+  // elected lane issues.
   if (warp == 0) {
-    if (lane == 0) {
-      // the pair's copies all count on the first CTA's barrier, which that CTA alone announces them to
-      const uint32_t full0 = CG == 2 ? map_rank(full(0), 0) : full(0);
-      const bool announce = CG == 1 || rank == 0;
-      int slot = 0, round = 0, issued = 0;
-      bool ok = true;
-      for (int i = cluster; i < total && ok; i += nclusters) {
-        const Tile t = tile_of<CG>(g, a, i);
-        const int nb = (t.n / CG + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = kABytes + nb * kBoxBytes;
-        const CUtensorMap* map_x = &a.map_x[nb - 1];
-        const int row = t.r0 + (CG == 2 ? (int)rank * (t.n / 2) : 0), ch = t.f0 + (CG == 2 ? (int)rank * 128 : 0);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (round > 0 && !role_wait(empty(slot), (round - 1) & 1, status, a.g.wait_ns, aborted)) {
-            ok = false;
-            break;
-          }
+    // the pair's copies all count on the first CTA's barrier, which that CTA alone announces them to
+    const uint32_t full0 = CG == 2 ? map_rank(full(0), 0) : full(0);
+    const bool announce = CG == 1 || rank == 0;
+    int slot = 0, round = 0, issued = 0;
+    bool ok = true;
+    for (int i = cluster; i < total && ok; i += nclusters) {
+      const Tile t = tile_of<CG>(g, a, i);
+      const int nb = (t.n / CG + kBoxRows - 1) / kBoxRows;
+      const uint32_t bytes = kABytes + nb * kBoxBytes;
+      const CUtensorMap* map_x = &a.map_x[nb - 1];
+      const int row = t.r0 + (CG == 2 ? (int)rank * (t.n / 2) : 0), ch = t.f0 + (CG == 2 ? (int)rank * 128 : 0);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = round == 0 || role_wait(empty(slot), (round - 1) & 1, status, a.g.wait_ns, aborted);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (elect_one()) {
           if (announce) mbar_expect_tx(full(slot), CG * bytes);
           bytes_s[slot] = bytes;
           const uint32_t dst = sbase + slot * stage_bytes;
           tma3<CG>(dst, &a.map_w, kb * kElem, ch, t.e, full0 + 8 * slot);
           tma2<CG>(dst + kABytes, map_x, kb * kElem, row, full0 + 8 * slot);
-          ++issued;
-          if (++slot == a.stages) {
-            slot = 0;
-            ++round;
-          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++slot == a.stages) {
+          slot = 0;
+          ++round;
         }
       }
-      issued_s = issued;
-      if (!ok) *aborted = 1;
-      // the last arrivals on this CTA's empty barriers land before it may exit
-      for (int u = max(0, issued - a.stages); u < issued && !*aborted; ++u)
-        if (!mbar_wait_fast(empty(u % a.stages), (u / a.stages) & 1, status, kDrainLimitNs)) *aborted = 1;
     }
+    if (lane == 0) issued_s = issued;
+    // the last arrivals on this CTA's empty barriers land before it may exit
+    for (int u = max(0, issued - a.stages); u < issued && ok; ++u)
+      ok = mbar_wait_fast(empty(u % a.stages), (u / a.stages) & 1, status, kDrainLimitNs);
+    if (!ok) *aborted = 1;
   } else if (warp == 1) {
-    if (lane == 0 && (CG == 1 || rank == 0)) {
+    if (CG == 1 || rank == 0) {
       int slot = 0, ph = 0, it = 0;
       bool ok = true;
       for (int i = cluster; i < total && ok; i += nclusters, ++it) {
         const Tile t = tile_of<CG>(g, a, i);
         const int buf = it & 1;
-        if (it >= 2 && !role_wait(acc_empty(buf), ((it >> 1) - 1) & 1, status, a.g.wait_ns, aborted)) {
-          ok = false;
-          break;
-        }
+        ok = it < 2 || role_wait(acc_empty(buf), ((it >> 1) - 1) & 1, status, a.g.wait_ns, aborted);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t idesc = a.idesc | ((uint32_t)(t.n >> 3) << 17);
         const uint32_t d = tmem + buf * kUnitCols;
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!role_wait(full(slot), ph, status, a.g.wait_ns, aborted)) {
-            ok = false;
-            break;
-          }
+          ok = role_wait(full(slot), ph, status, a.g.wait_ns, aborted);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc_fence_after();
-          const uint64_t ad = sw128_desc(sbase + slot * stage_bytes), bd = sw128_desc(sbase + slot * stage_bytes + kABytes);
+          if (elect_one()) {
+            const uint64_t ad = sw128_desc(sbase + slot * stage_bytes), bd = sw128_desc(sbase + slot * stage_bytes + kABytes);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_ss<CG, I8>(d, ad + 2 * k, bd + 2 * k, idesc, kb > kb0 || k > 0);
-          commit<CG>(empty(slot));
+            for (int k = 0; k < 4; ++k) mma_ss<CG, I8>(d, ad + 2 * k, bd + 2 * k, idesc, kb > kb0 || k > 0);
+            commit<CG>(empty(slot));
+            if (kb == kb1 - 1) commit<CG>(acc_full(buf));
+          }
+          __syncwarp();
           if (++slot == a.stages) {
             slot = 0;
             ph ^= 1;
           }
         }
-        if (ok) commit<CG>(acc_full(buf));
       }
       if (!ok) *aborted = 1;
       // every MMA completes before the cluster frees its TMEM
-      if constexpr (CG == 1) mma_commit(drained);
-      else
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(drained) : "memory");
+      if (elect_one()) {
+        if constexpr (CG == 1) mma_commit(drained);
+        else
+          asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(drained) : "memory");
+      }
+      __syncwarp();
       mbar_wait(drained, 0, status, kDrainLimitNs);
     }
   } else {
