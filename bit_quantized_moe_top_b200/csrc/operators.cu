@@ -79,6 +79,7 @@ moe_status_t moe_block_norm(const moe_block_norm_t* p, void* cuda_stream) {
   a.w_pre = p->pre_weight;
   a.eps = p->eps;
   a.w_off = p->weight_offset;
+  a.inv_K = 1.f / p->width;
   a.r_out = p->residual_out;
   a.ldro = p->residual_out_stride;
   a.h = p->h;

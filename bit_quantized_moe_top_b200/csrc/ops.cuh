@@ -26,7 +26,7 @@ struct NormArgs {
   long long ldr;
   float res_scale, br_scale;
   const void* w_pre;
-  float eps, w_off;
+  float eps, w_off, inv_K;
   void* r_out;
   long long ldro;
   void* h;
