@@ -316,29 +316,31 @@ def moe_layer_destroy(layer: int) -> None:
 # stand-alone operators around the experts
 # ---------------------------------------------------------------------------
 
+# The checks below are written for short calls: one condition per tensor, device
+# indices as integers, no temporary views.
+
+_DTYPES = {}
+
+
+def _dtypes() -> dict:
+    """The library's codes of the torch dtypes."""
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
+    return _DTYPES
+
+
 def _require(ok, where: str):
     if not ok:
         raise MoEError(1, where)
 
 
-_DTYPES = {}
-
-
-def _dtype(t) -> int:
-    """The library's code of a torch dtype, or -1."""
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
-    return _DTYPES.get(t, -1)
-
-
-def _call(device, stream, where: str, fn, *args) -> None:
-    """fn(*args, stream) with ``device`` current, on its current stream unless one is given."""
+def _call(index: int, stream, where: str, fn, *args) -> None:
+    """fn(*args, stream) with device ``index`` current, on its current stream unless one is given."""
     import torch
-    index = device.index
     if stream is None:
-        stream = torch.cuda.current_stream(index).cuda_stream
-    if index == torch.cuda.current_device():
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch._C._cuda_getDevice():
         status = fn(*args, stream)
     else:
         with torch.cuda.device(index):
@@ -347,15 +349,22 @@ def _call(device, stream, where: str, fn, *args) -> None:
         raise MoEError(status, where)
 
 
-def _rows(t, where: str, device, n=None, width=None) -> int:
-    """Row stride of a 2-D tensor whose rows are contiguous; checks shape and device."""
-    _require(t.dim() == 2 and t.device == device and (t.stride(1) == 1 or t.shape[1] == 1), where)
-    _require((n is None or t.shape[0] == n) and (width is None or t.shape[1] == width), where)
-    return t.stride(0)
+def _rows(t, where: str, index: int, n, width: int) -> int:
+    """Row stride of a 2-D tensor [n (None: any), width] on device ``index`` whose rows are contiguous."""
+    if t.dim() != 2 or t.get_device() != index:
+        raise MoEError(1, where)
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if cols != width or (unit != 1 and cols != 1) or (n is not None and rows != n):
+        raise MoEError(1, where)
+    return ld
 
 
-def _flat(t, where: str, device, dtype, *shape) -> None:
-    _require(t.device == device and t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous(), where)
+def _flat(t, where: str, index: int, dtype, shape) -> int:
+    """Address of a contiguous tensor of the given type, shape and device."""
+    if t.get_device() != index or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise MoEError(1, where)
+    return t.data_ptr()
 
 
 def moe_block_norm(residual=None, branch=None, *, w_pre=None, w_post=None, gate=None, gate_sigmoid: bool = False,
@@ -372,66 +381,57 @@ def moe_block_norm(residual=None, branch=None, *, w_pre=None, w_post=None, gate=
     ``residual`` itself."""
     import torch
     f = "moe_block_norm"
-    _require(residual is not None or branch is not None, f)
     lead = residual if residual is not None else branch
-    device = lead.device
-    _require(lead.is_cuda and lead.dim() == 2, f)
-    K = lead.shape[1]
-    if residual is not None:
-        T = residual.shape[0]
-    else:
-        T = branch.shape[0] if inv_pos is None else inv_pos.shape[0]
-    if branch is not None:
-        dt = branch.dtype
-    elif w_pre is not None:
-        dt = w_pre.dtype
-    else:
-        dt = residual.dtype
+    _require(lead is not None and lead.dim() == 2 and lead.is_cuda, f)
+    index = lead.get_device()
+    T, K = lead.shape
+    if residual is None and inv_pos is not None:
+        T = inv_pos.shape[0]
+    dt = branch.dtype if branch is not None else w_pre.dtype if w_pre is not None else residual.dtype
     if residual_out is None and branch is not None:
-        residual_out = torch.empty((T, K), dtype=dt if residual is None else residual.dtype, device=device)
+        residual_out = lead.new_empty((T, K)) if residual is not None else torch.empty((T, K), dtype=dt, device=lead.device)
     if h_out is None and w_pre is not None:
-        h_out = torch.empty((T, K), dtype=dt, device=device)
-    a = BlockNormArgs(tokens=T, width=K, dtype=_dtype(dt), residual_scale=residual_scale, branch_scale=branch_scale,
-                      eps=eps, weight_offset=weight_offset, gate_sigmoid=1 if gate_sigmoid else 0)
-    rdt = residual.dtype if residual is not None else (residual_out.dtype if residual_out is not None else dt)
-    a.residual_dtype = _dtype(rdt)
+        h_out = torch.empty((T, K), dtype=dt, device=lead.device)
+    rdt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else dt
+    codes = _dtypes()
+    a = BlockNormArgs(T, K, codes.get(dt, -1), codes.get(rdt, -1))
+    a.residual_scale, a.branch_scale, a.eps, a.weight_offset = residual_scale, branch_scale, eps, weight_offset
     if residual is not None:
-        a.residual, a.residual_stride = residual.data_ptr(), _rows(residual, f, device)
+        a.residual_stride = _rows(residual, f, index, T, K)
+        a.residual = residual.data_ptr()
     if branch is not None:
-        a.branch_stride = _rows(branch, f, device, None if inv_pos is not None else T, K)
+        a.branch_stride = _rows(branch, f, index, T if inv_pos is None else None, K)
         a.branch, a.branch_rows = branch.data_ptr(), branch.shape[0]
     if inv_pos is not None or pair_weights is not None:
-        _require(inv_pos is not None and pair_weights is not None and inv_pos.dim() == 2, f)
-        k = inv_pos.shape[1]
-        _flat(inv_pos, f, device, torch.int32, T, k)
-        _flat(pair_weights, f, device, torch.float32, T, k)
-        _require(k >= 1, f)
-        a.inv_pos, a.pair_weights, a.pairs = inv_pos.data_ptr(), pair_weights.data_ptr(), k
+        _require(inv_pos is not None and pair_weights is not None and inv_pos.dim() == 2 and inv_pos.shape[1] >= 1, f)
+        a.pairs = k = inv_pos.shape[1]
+        a.inv_pos = _flat(inv_pos, f, index, torch.int32, (T, k))
+        a.pair_weights = _flat(pair_weights, f, index, torch.float32, (T, k))
     if w_post is not None:
-        _flat(w_post, f, device, dt, K)
-        a.post_weight = w_post.data_ptr()
+        a.post_weight = _flat(w_post, f, index, dt, (K,))
     if w_pre is not None:
-        _flat(w_pre, f, device, dt, K)
-        a.pre_weight = w_pre.data_ptr()
+        a.pre_weight = _flat(w_pre, f, index, dt, (K,))
     if gate is not None:
-        _require(gate.device == device and gate.dtype == dt, f)
         if gate.dim() == 1:
-            _flat(gate, f, device, dt, K)
-            a.gate_token_stride, a.gate_channel_stride = 0, 1
+            a.gate = _flat(gate, f, index, dt, (K,))
+            a.gate_channel_stride = 1
         else:
-            _require(gate.dim() == 2 and gate.shape[0] == T and gate.shape[1] in (1, K), f)
-            a.gate_channel_stride = 0 if gate.shape[1] == 1 else 1
-            _require(a.gate_channel_stride == 0 or gate.stride(1) == 1, f)
-            a.gate_token_stride = gate.stride(0)
-        a.gate = gate.data_ptr()
+            width = gate.shape[1]
+            _require(gate.dtype is dt and (width == 1 or width == K), f)
+            a.gate_token_stride = _rows(gate, f, index, T, width)
+            a.gate_channel_stride = 0 if width == 1 else 1
+            a.gate = gate.data_ptr()
+        a.gate_sigmoid = 1 if gate_sigmoid else 0
     if residual_out is not None:
-        _require(residual_out.dtype == rdt, f)
-        a.residual_out, a.residual_out_stride = residual_out.data_ptr(), _rows(residual_out, f, device, T, K)
+        _require(residual_out.dtype is rdt, f)
+        a.residual_out_stride = _rows(residual_out, f, index, T, K)
+        a.residual_out = residual_out.data_ptr()
     if h_out is not None:
-        _require(h_out.dtype == dt, f)
-        a.h, a.h_stride = h_out.data_ptr(), _rows(h_out, f, device, T, K)
+        _require(h_out.dtype is dt, f)
+        a.h_stride = _rows(h_out, f, index, T, K)
+        a.h = h_out.data_ptr()
     if T > 0:
-        _call(device, stream, f, _lib().moe_block_norm, ctypes.byref(a))
+        _call(index, stream, f, _lib().moe_block_norm, ctypes.byref(a))
     return residual_out, h_out
 
 
@@ -440,40 +440,54 @@ def moe_quantize_rows(x, src_rows=None, codes=None, scales=None, stream: Optiona
     as 8-bit codes with one scale each; returns (codes int8 [R, K], scales fp32 [R])."""
     import torch
     f = "moe_quantize_rows"
-    _require(x.is_cuda, f)
-    ldx = _rows(x, f, x.device)
+    _require(x.dim() == 2 and x.is_cuda, f)
+    index = x.get_device()
     M, K = x.shape
-    R = M
+    ldx = _rows(x, f, index, M, K)
+    R, src = M, None
     if src_rows is not None:
+        _require(src_rows.dim() == 1, f)
         R = src_rows.shape[0]
-        _flat(src_rows, f, x.device, torch.int32, R)
+        src = _flat(src_rows, f, index, torch.int32, (R,))
     if codes is None:
-        codes = torch.empty((R, K), dtype=torch.int8, device=x.device)
+        codes, ldq = torch.empty((R, K), dtype=torch.int8, device=x.device), K
+    else:
+        _require(codes.dtype is torch.int8, f)
+        ldq = _rows(codes, f, index, R, K)
     if scales is None:
         scales = torch.empty((R,), dtype=torch.float32, device=x.device)
-    _require(codes.dtype == torch.int8, f)
-    _flat(scales, f, x.device, torch.float32, R)
-    _call(x.device, stream, f, _lib().moe_quantize_rows, x.data_ptr(), ldx, M, _dtype(x.dtype), _ptr(src_rows), R, K,
-          codes.data_ptr(), _rows(codes, f, x.device, R, K), scales.data_ptr())
+    sp = _flat(scales, f, index, torch.float32, (R,))
+    _call(index, stream, f, _lib().moe_quantize_rows, x.data_ptr(), ldx, M, _dtypes().get(x.dtype, -1), src, R, K,
+          codes.data_ptr(), ldq, sp)
     return codes, scales
 
 
 def _product(f, x, w, offsets, out_dtype, out):
-    """Checks of the grouped products: (row stride, weight strides, E, K, N, out)."""
+    """Checks of the grouped products and their common arguments."""
     import torch
-    _require(x.is_cuda and w.dtype == x.dtype and w.device == x.device, f)
-    ldx = _rows(x, f, x.device)
+    if x.dim() != 2 or not x.is_cuda or w.dtype is not x.dtype or w.get_device() != x.get_device():
+        raise MoEError(1, f)
+    index = x.get_device()
     R, K = x.shape
-    if w.dim() == 2:
-        w = w.unsqueeze(0)
-    _require(w.dim() == 3 and w.shape[2] == K and (w.stride(2) == 1 or K == 1), f)
-    E, N = w.shape[0], w.shape[1]
+    ldx = _rows(x, f, index, R, K)
+    shape, strides = w.shape, w.stride()
+    if len(shape) == 2:
+        E, N = 1, shape[0]
+        ldw, ldwe = strides[0], 0
+    else:
+        _require(len(shape) == 3, f)
+        E, N = shape[0], shape[1]
+        ldwe, ldw = strides[0], strides[1]
+    _require(shape[-1] == K and (strides[-1] == 1 or K == 1), f)
+    off = None
     if offsets is not None:
-        _flat(offsets, f, x.device, torch.int32, E + 1)
+        off = _flat(offsets, f, index, torch.int32, (E + 1,))
     if out is None:
-        out = torch.empty((R, N), dtype=out_dtype, device=x.device)
-    _require(out_dtype is None or out.dtype == out_dtype, f)
-    return ldx, w.stride(1), w.stride(0), R, E, K, N, out, _rows(out, f, x.device, R, N)
+        out, ldy = torch.empty((R, N), dtype=out_dtype, device=x.device), N
+    else:
+        _require(out_dtype is None or out.dtype is out_dtype, f)
+        ldy = _rows(out, f, index, R, N)
+    return index, ldx, ldw, ldwe, off, R, E, K, N, out, ldy
 
 
 def moe_int8_matmul(x, row_scales, w, channel_scales, offsets=None, out_dtype=None, out=None,
@@ -485,14 +499,14 @@ def moe_int8_matmul(x, row_scales, w, channel_scales, offsets=None, out_dtype=No
     range are left as they were. out_dtype: bf16 (default), fp16 or fp32."""
     import torch
     f = "moe_int8_matmul"
-    _require(x.dtype == torch.int8, f)
-    ldx, ldw, ldwe, R, E, K, N, out, ldy = _product(f, x, w, offsets, out_dtype or (torch.bfloat16 if out is None else None),
-                                                    out)
-    _flat(row_scales, f, x.device, torch.float32, R)
-    _require(channel_scales.numel() == E * N, f)
-    _flat(channel_scales, f, x.device, torch.float32, *w.shape[:-1])
-    _call(x.device, stream, f, _lib().moe_int8_matmul, x.data_ptr(), ldx, row_scales.data_ptr(), w.data_ptr(), ldw,
-          ldwe, channel_scales.data_ptr(), _ptr(offsets), R, E, K, N, out.data_ptr(), ldy, _dtype(out.dtype))
+    _require(x.dtype is torch.int8, f)
+    if out is None and out_dtype is None:
+        out_dtype = torch.bfloat16
+    index, ldx, ldw, ldwe, off, R, E, K, N, out, ldy = _product(f, x, w, offsets, out_dtype, out)
+    xs = _flat(row_scales, f, index, torch.float32, (R,))
+    ws = _flat(channel_scales, f, index, torch.float32, w.shape[:-1])
+    _call(index, stream, f, _lib().moe_int8_matmul, x.data_ptr(), ldx, xs, w.data_ptr(), ldw, ldwe, ws, off, R, E, K, N,
+          out.data_ptr(), ldy, _dtypes().get(out.dtype, -1))
     return out
 
 
@@ -501,9 +515,12 @@ def moe_grouped_matmul(x, w, offsets=None, out_dtype=None, out=None, stream: Opt
     order and experts w [E, N, K] (or [N, K]); offsets as for moe_int8_matmul.
     out_dtype: bf16, fp16 or fp32 (default: x's)."""
     f = "moe_grouped_matmul"
-    ldx, ldw, ldwe, R, E, K, N, out, ldy = _product(f, x, w, offsets, out_dtype or (x.dtype if out is None else None), out)
-    _call(x.device, stream, f, _lib().moe_grouped_matmul, x.data_ptr(), ldx, w.data_ptr(), ldw, ldwe, _ptr(offsets), R,
-          E, K, N, _dtype(x.dtype), out.data_ptr(), ldy, _dtype(out.dtype))
+    if out is None and out_dtype is None:
+        out_dtype = x.dtype
+    index, ldx, ldw, ldwe, off, R, E, K, N, out, ldy = _product(f, x, w, offsets, out_dtype, out)
+    codes = _dtypes()
+    _call(index, stream, f, _lib().moe_grouped_matmul, x.data_ptr(), ldx, w.data_ptr(), ldw, ldwe, off, R, E, K, N,
+          codes.get(x.dtype, -1), out.data_ptr(), ldy, codes.get(out.dtype, -1))
     return out
 
 
