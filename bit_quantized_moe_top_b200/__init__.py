@@ -316,8 +316,9 @@ def moe_layer_destroy(layer: int) -> None:
 # stand-alone operators around the experts
 # ---------------------------------------------------------------------------
 
-# The checks below are written for short calls: one condition per tensor, device
-# indices as integers, no temporary views.
+# The checks below are written for short calls (of a one-token call they are
+# most of the time): the usual case, a contiguous tensor of the expected shape,
+# is looked at first, outputs made here are not checked, and no views are made.
 
 _DTYPES = {}
 
@@ -351,7 +352,11 @@ def _call(index: int, stream, where: str, fn, *args) -> None:
 
 def _rows(t, where: str, index: int, n, width: int) -> int:
     """Row stride of a 2-D tensor [n (None: any), width] on device ``index`` whose rows are contiguous."""
-    if t.dim() != 2 or t.get_device() != index:
+    if t.get_device() != index:
+        raise MoEError(1, where)
+    if t.is_contiguous() and t.shape == (n, width):
+        return width
+    if t.dim() != 2:
         raise MoEError(1, where)
     rows, cols = t.shape
     ld, unit = t.stride()
@@ -388,10 +393,6 @@ def moe_block_norm(residual=None, branch=None, *, w_pre=None, w_post=None, gate=
     if residual is None and inv_pos is not None:
         T = inv_pos.shape[0]
     dt = branch.dtype if branch is not None else w_pre.dtype if w_pre is not None else residual.dtype
-    if residual_out is None and branch is not None:
-        residual_out = lead.new_empty((T, K)) if residual is not None else torch.empty((T, K), dtype=dt, device=lead.device)
-    if h_out is None and w_pre is not None:
-        h_out = torch.empty((T, K), dtype=dt, device=lead.device)
     rdt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else dt
     codes = _dtypes()
     a = BlockNormArgs(T, K, codes.get(dt, -1), codes.get(rdt, -1))
@@ -399,6 +400,23 @@ def moe_block_norm(residual=None, branch=None, *, w_pre=None, w_post=None, gate=
     if residual is not None:
         a.residual_stride = _rows(residual, f, index, T, K)
         a.residual = residual.data_ptr()
+    # a new output is like the contiguous residual, whose copy costs least
+    like = residual if residual is not None and residual.is_contiguous() else None
+    if residual_out is not None:
+        _require(residual_out.dtype is rdt, f)
+        a.residual_out_stride = _rows(residual_out, f, index, T, K)
+        a.residual_out = residual_out.data_ptr()
+    elif branch is not None:
+        residual_out = torch.empty_like(like) if like is not None else torch.empty((T, K), dtype=rdt, device=lead.device)
+        a.residual_out_stride, a.residual_out = K, residual_out.data_ptr()
+    if h_out is not None:
+        _require(h_out.dtype is dt, f)
+        a.h_stride = _rows(h_out, f, index, T, K)
+        a.h = h_out.data_ptr()
+    elif w_pre is not None:
+        h_out = (torch.empty_like(like, dtype=dt) if like is not None else
+                 torch.empty((T, K), dtype=dt, device=lead.device))
+        a.h_stride, a.h = K, h_out.data_ptr()
     if branch is not None:
         a.branch_stride = _rows(branch, f, index, T if inv_pos is None else None, K)
         a.branch, a.branch_rows = branch.data_ptr(), branch.shape[0]
@@ -422,14 +440,6 @@ def moe_block_norm(residual=None, branch=None, *, w_pre=None, w_post=None, gate=
             a.gate_channel_stride = 0 if width == 1 else 1
             a.gate = gate.data_ptr()
         a.gate_sigmoid = 1 if gate_sigmoid else 0
-    if residual_out is not None:
-        _require(residual_out.dtype is rdt, f)
-        a.residual_out_stride = _rows(residual_out, f, index, T, K)
-        a.residual_out = residual_out.data_ptr()
-    if h_out is not None:
-        _require(h_out.dtype is dt, f)
-        a.h_stride = _rows(h_out, f, index, T, K)
-        a.h = h_out.data_ptr()
     if T > 0:
         _call(index, stream, f, _lib().moe_block_norm, ctypes.byref(a))
     return residual_out, h_out
@@ -450,13 +460,15 @@ def moe_quantize_rows(x, src_rows=None, codes=None, scales=None, stream: Optiona
         R = src_rows.shape[0]
         src = _flat(src_rows, f, index, torch.int32, (R,))
     if codes is None:
-        codes, ldq = torch.empty((R, K), dtype=torch.int8, device=x.device), K
+        codes, ldq = torch.empty(R, K, dtype=torch.int8, device=x.device), K
     else:
         _require(codes.dtype is torch.int8, f)
         ldq = _rows(codes, f, index, R, K)
     if scales is None:
-        scales = torch.empty((R,), dtype=torch.float32, device=x.device)
-    sp = _flat(scales, f, index, torch.float32, (R,))
+        scales = torch.empty(R, dtype=torch.float32, device=x.device)
+        sp = scales.data_ptr()
+    else:
+        sp = _flat(scales, f, index, torch.float32, (R,))
     _call(index, stream, f, _lib().moe_quantize_rows, x.data_ptr(), ldx, M, _dtypes().get(x.dtype, -1), src, R, K,
           codes.data_ptr(), ldq, sp)
     return codes, scales
@@ -483,7 +495,7 @@ def _product(f, x, w, offsets, out_dtype, out):
     if offsets is not None:
         off = _flat(offsets, f, index, torch.int32, (E + 1,))
     if out is None:
-        out, ldy = torch.empty((R, N), dtype=out_dtype, device=x.device), N
+        out, ldy = torch.empty(R, N, dtype=out_dtype, device=x.device), N
     else:
         _require(out_dtype is None or out.dtype is out_dtype, f)
         ldy = _rows(out, f, index, R, N)
