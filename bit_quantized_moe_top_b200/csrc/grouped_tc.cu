@@ -52,6 +52,8 @@ struct TcArgs {
   GroupedArgs g;
   uint32_t idesc;      // without the N field
   int NF;              // channel tiles
+  uint32_t nf_inv;     // 2^32 / NF, rounded down, + 1
+  int unit;            // step of a tile's rows
   int nmax;            // rows per tile
   int stages, bslot;   // ring depth, bytes of a stage's x part
   int S;               // CTAs splitting K (CG = 1)
@@ -85,6 +87,9 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
 __device__ __forceinline__ void complete_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
 }
@@ -95,6 +100,10 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 }
 // makes what other CTAs of the cluster wrote before their arrivals visible
 __device__ __forceinline__ void fence_acquire_cluster() { asm volatile("fence.acq_rel.cluster;\n" ::: "memory"); }
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 
 // ---- tcgen05 and TMA forms of one CTA or a CTA pair
 template <int CG>
@@ -168,21 +177,25 @@ struct Tile {
 // as many distinct weight rows as activation rows.
 template <int CG>
 __device__ __forceinline__ Tile tile_of(const GroupTable& g, const TcArgs& a, int i) {
-  constexpr int kUnit = 16 * CG;
+  // i / NF by a product that is one too large at most
+  auto by_nf = [&](int v) {
+    const int q = a.NF == 1 ? v : (int)__umulhi((uint32_t)v, a.nf_inv);
+    return q * a.NF > v ? q - 1 : q;
+  };
   Tile t;
-  t.e = find_group(g, a.g.E, i / a.NF);
+  t.e = find_group(g, a.g.E, by_nf(i));
   const int nt = g.first[t.e + 1] - g.first[t.e], rows = g.rows[t.e];
   const int local = i - g.first[t.e] * a.NF;
-  const int band = local / (kBandTc * a.NF), in = local - band * kBandTc * a.NF;
+  const int band = by_nf(local) / kBandTc, in = local - band * kBandTc * a.NF;
   const int bt = min(kBandTc, nt - band * kBandTc);
-  const int f = in / bt, tk = band * kBandTc + in - f * bt;
-  // widths in MMA units that differ by one at most, so that no tile reads its
+  const int f = bt == 1 ? in : in / bt, tk = band * kBandTc + in - f * bt;
+  // widths in units that differ by one at most, so that no tile reads its
   // weights for a few rows only
-  const int units = (rows + kUnit - 1) / kUnit, base = units / nt, more = units - base * nt;
+  const int units = (rows + a.unit - 1) / a.unit, base = nt == 1 ? units : units / nt, more = units - base * nt;
   const int u0 = tk * base + min(tk, more);
-  t.n = (base + (tk < more ? 1 : 0)) * kUnit;
-  t.live = min(t.n, rows - u0 * kUnit);
-  t.r0 = g.begin[t.e] + u0 * kUnit;
+  t.n = (base + (tk < more ? 1 : 0)) * a.unit;
+  t.live = min(t.n, rows - u0 * a.unit);
+  t.r0 = g.begin[t.e] + u0 * a.unit;
   t.f0 = f * 128 * CG;
   return t;
 }
@@ -329,13 +342,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
     issued_s = 0;
     fence_barrier_init();
   }
+  if (warp == 0 && elect_one()) {
+    prefetch_map(&a.map_w);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) prefetch_map(&a.map_x[b]);
+  }
   if (warp == 1) alloc_tmem<CG>(smem_u32(&tmem_slot), kCols);
-  pdl_wait();
-  pdl_trigger();
-  build_group_table(g, a.g.offsets, a.g.rows, a.g.E, RowTilesTc{a.nmax});
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
+  pdl_wait();  // what precedes touches no memory of the call
+  pdl_trigger();
+  build_group_table(g, a.g.offsets, a.g.rows, a.g.E, RowTilesTc{a.nmax});
   const uint32_t tmem = tmem_slot;
   const int total = g.first[a.g.E] * a.NF;
   const int nk = (a.g.K + kElem - 1) / kElem;
@@ -464,16 +482,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
           else mbar_arrive(acc_empty(buf));
         }
       } else {
-        // partial sums of columns [q c, q c + c) go to CTA q, slot [rank]
+        // Partial sums of columns [q c, q c + c) go to CTA q, slot [rank]; in
+        // a slot four columns of a channel lie together, 16 bytes a lane.
         const int c = t.n / a.S;
-        const uint32_t part = smem_u32(tail) + (uint32_t)(((int)rank * c) * 128 + quarter * 32 + lane) * 4;
+        const uint32_t part = smem_u32(tail) + (uint32_t)((int)rank * c * 512 + (quarter * 32 + lane) * 16);
         for (int c0 = half * 16; c0 < t.n; c0 += 32) {
           uint32_t v[16];
           tmem_ld16(d + c0, v);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
+          for (int j = 0; j < 16; j += 4) {
             const int q = (c0 + j) / c;
-            st_cluster_u32(map_rank(part + (uint32_t)(c0 + j - q * c) * 512, q), v[j]);
+            st_cluster_v4(map_rank(part + (uint32_t)(c0 + j - q * c) * 512, q), v + j);
           }
         }
         __syncwarp();
@@ -484,21 +503,42 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
           *aborted = 1;
           break;
         }
-        const uint32_t* sums = reinterpret_cast<const uint32_t*>(tail) + quarter * 32 + lane;
-        for (int j = half; j < c; j += 2) {
+        // this CTA's c columns, four at a time: added in rank order, finished, stored
+        const uint4* sums = reinterpret_cast<const uint4*>(tail) + quarter * 32 + lane;
+        const int slot4 = c * 32;  // 16-byte words of a slot
+        for (int j = half * 4; j < c; j += 8) {
           const int col = (int)rank * c + j;
           if (col >= t.live || ch >= a.g.N) break;
-          float y;
+          float y[4];
           if constexpr (I8) {
-            int s = 0;
-            for (int q = 0; q < a.S; ++q) s += (int)sums[(q * c + j) * 128];
-            y = (float)s * (ws * a.g.xs[t.r0 + col]);
+            int n[4] = {};
+            for (int q = 0; q < a.S; q += 2) {
+              const uint4 u = sums[q * slot4 + j * 32], w = sums[(q + 1) * slot4 + j * 32];
+              n[0] += (int)u.x + (int)w.x;
+              n[1] += (int)u.y + (int)w.y;
+              n[2] += (int)u.z + (int)w.z;
+              n[3] += (int)u.w + (int)w.w;
+            }
+#pragma unroll
+            for (int h = 0; h < 4; ++h) y[h] = col + h < t.live ? (float)n[h] * (ws * a.g.xs[t.r0 + col + h]) : 0.f;
           } else {
-            float s = 0.f;
-            for (int q = 0; q < a.S; ++q) s += __uint_as_float(sums[(q * c + j) * 128]);
-            y = s;
+            float4 n = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int q = 0; q < a.S; q += 2) {
+              const uint4 u = sums[q * slot4 + j * 32], w = sums[(q + 1) * slot4 + j * 32];
+              n.x = n.x + __uint_as_float(u.x) + __uint_as_float(w.x);
+              n.y = n.y + __uint_as_float(u.y) + __uint_as_float(w.y);
+              n.z = n.z + __uint_as_float(u.z) + __uint_as_float(w.z);
+              n.w = n.w + __uint_as_float(u.w) + __uint_as_float(w.w);
+            }
+            y[0] = n.x;
+            y[1] = n.y;
+            y[2] = n.z;
+            y[3] = n.w;
           }
-          static_cast<TO*>(a.g.y)[(long long)(t.r0 + col) * a.g.ldy + ch] = from_f32<TO>(y);
+          TO* out = static_cast<TO*>(a.g.y) + (long long)(t.r0 + col) * a.g.ldy + ch;
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            if (col + h < t.live) out[h * a.g.ldy] = from_f32<TO>(y[h]);
         }
       }
     }
@@ -526,7 +566,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
     cluster_sync();
   }
   if (warp == 1) free_tmem<CG>(tmem, kCols);
-  cluster_sync();
+  if constexpr (CG == 2) cluster_sync();  // the pair's TMEM goes together
 }
 
 // ---------------------------------------------------------------------------
@@ -630,30 +670,64 @@ cudaError_t launch_grouped_tc(const GroupedArgs& g, int op, int y_dtype, cudaStr
   a.idesc = op == kOpInt8 ? (2u << 4) | (1u << 7) | (1u << 10)
                           : (1u << 4) | ((op == DT_BF16 ? 1u : 0u) << 7) | ((op == DT_BF16 ? 1u : 0u) << 10);
   const int nk = (g.K * es + kRowBytes - 1) / kRowBytes;
-  // row tiles: at most one partial tile per group that can have rows
+  // Tile width and form. Groups are taken as equally large (their sizes are
+  // only known on the device). What a tile takes per 128 bytes of K is the
+  // larger of its MMAs, 2 cycles a row, and of the L2 reads of its CTA's 128
+  // channels and n / CG rows at about 55 bytes a cycle (measured: 8192 x 4096 x
+  // 4096 at 55, 12288 x 2048 x 2816 in 32 groups at 51), so narrower tiles cost
+  // nearly as much as wide ones, and it is the number of tiles that a CTA works
+  // off one after the other that counts. The split of K (CG = 1) pays an
+  // exchange of the partial sums, about 3500 cycles and 40 a column.
   const long long groups = std::min<long long>(g.rows, g.E);
-  const long long wide = (groups + g.rows / 256) * ((g.N + 255) / 256);
-  if (wide > pairs || g.rows > 128 * g.E) {
-    a.idesc |= (uint32_t)(256 >> 4) << 24;
-    a.NF = (g.N + 255) / 256;
-    a.nmax = 256;
-    a.S = 1;
+  const long long mean = (g.rows + groups - 1) / groups;
+  const long long streamed = groups * g.N * nk * kRowBytes / 3500;  // weights at HBM's bytes per cycle
+  auto tiles_of = [&](int cg, int width) { return groups * ((mean + width - 1) / width) * ((g.N + 128 * cg - 1) / (128 * cg)); };
+  auto cost_of = [&](int cg, int width, int S) {
+    const long long nt = (mean + width - 1) / width, unit = cg == 2 || S == 8 ? 32 : 16;
+    const long long n = ((mean + nt - 1) / nt + unit - 1) / unit * unit;
+    const long long per_k = std::max(2 * n, (128 + n / cg) * kRowBytes / 55);
+    const long long slots = cg == 2 ? pairs : sms / S, waves = (tiles_of(cg, width) + slots - 1) / slots;
+    return std::max(waves * ((nk + S - 1) / S) * per_k, streamed) + (S > 1 ? 3500 + 40 * n : 0);
+  };
+  int cg = 2, width = 256, S = 1;
+  long long best = cost_of(2, 256, 1);
+  auto consider = [&](int c, int w, int s) {
+    const long long cost = cost_of(c, w, s);
+    if (cost < best) {
+      best = cost;
+      cg = c;
+      width = w;
+      S = s;
+    }
+  };
+  for (int w = 224; w >= 64; w -= 32) consider(2, w, 1);
+  // few tiles: single CTAs, split along K while there are CTAs for it
+  for (int w = 128; w >= 16; w /= 2) {
+    if (mean <= w / 2 && w > 16) continue;
+    const long long tiles = groups * ((g.N + 127) / 128) * ((mean + w - 1) / w);
+    for (int s = 1; s <= 8 && tiles * s <= sms; s *= 2)
+      if (s == 1 || nk >= s * 2) consider(1, w, s);
+  }
+  a.NF = (g.N + 128 * cg - 1) / (128 * cg);
+  a.nf_inv = (uint32_t)((1ull << 32) / a.NF + 1);
+  a.unit = cg == 2 || S == 8 ? 32 : 16;
+  a.nmax = std::max(width, a.unit);
+  a.S = S;
+  a.idesc |= (uint32_t)(128 * cg >> 4) << 24;
+  // ceil(r / n) summed over the groups' rows r: at most one tile for each of
+  // them and one for every n of the other rows
+  const long long most = (groups + (g.rows - groups) / a.nmax) * a.NF;
+  if (cg == 2) {
     a.bslot = 128 * kRowBytes;
     a.stages = 6;
     const size_t smem = (size_t)a.stages * (kABytes + a.bslot) + kStagingBytes + 1024;
-    return launch_tc_typed<2>(a, op, y_dtype, (int)std::min<long long>(wide, pairs), smem, st);
+    return launch_tc_typed<2>(a, op, y_dtype, (int)std::min<long long>(most, pairs), smem, st);
   }
-  a.idesc |= (uint32_t)(128 >> 4) << 24;
-  a.NF = (g.N + 127) / 128;
-  a.nmax = std::min(128, (g.rows + 15) / 16 * 16);
-  const long long tiles = (groups + g.rows / a.nmax) * a.NF;
-  a.S = 1;
-  while (a.S < 8 && tiles * a.S * 2 <= sms && nk >= a.S * 4) a.S *= 2;
   a.bslot = (a.nmax + kBoxRows - 1) / kBoxRows * kBoxBytes;
   const int fixed = (a.S > 1 ? a.nmax * 512 : kStagingBytes) + 1024;
   a.stages = std::min({kMaxStagesTc, (kSmemBudget - fixed) / (kABytes + a.bslot), std::max(2, (nk + a.S - 1) / a.S)});
   const size_t smem = (size_t)a.stages * (kABytes + a.bslot) + fixed;
-  const int clusters = (int)(a.S > 1 ? tiles : std::min<long long>(tiles, sms));
+  const int clusters = (int)(a.S > 1 ? most : std::min<long long>(most, sms));
   return launch_tc_typed<1>(a, op, y_dtype, clusters, smem, st);
 }
 
