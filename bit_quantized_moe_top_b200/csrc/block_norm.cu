@@ -167,14 +167,23 @@ __device__ __forceinline__ int row_shift(const void* row) {
   return (int)(reinterpret_cast<uintptr_t>(row) / ES) & 7;
 }
 
+// How a call's rows lie: kFull, aligned and with a vector for every thread and
+// nothing over (no bounds to look at: norm of 16384 x 2048 46 -> 44 us,
+// quantiser of 8192 x 4096 18 -> 16 us); kEven, aligned; kShift, any.
+enum : int { kFull, kEven, kShift };
+
 // One row per threadIdx.y, NV vectors of 8 elements per thread. Every load that
 // does not wait for a reduction is issued before the first one, so that a row
 // waits for HBM once; the weights, which every row reads, come from the caches.
-// (Shifted rows of more than 4096 elements go two vectors at a time and read
-// the residual late instead: their loads take twice the registers.)
-template <typename T, typename RT, int NV, bool SHIFT>
-__global__ void __launch_bounds__(NV == 1 ? 1024 : NV == 4 && SHIFT ? 544 : 512)
+// (Shifted rows of more than 8192 elements go two vectors at a time and read
+// the residual late instead, since their loads take twice the registers, and
+// keep to 56 registers, so that two blocks share an SM and one's loads run
+// under the other's reductions: 4096 rows of 9001 with two combined rows 168
+// -> 133 us in spite of the spills.)
+template <typename T, typename RT, int NV, int FORM>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : NV == 4 && FORM == kShift ? 544 : 512, (NV == 4 && FORM == kShift) || (NV == 2 && FORM != kShift) ? 2 : 1)
     block_norm_kernel(const __grid_constant__ NormArgs a) {
+  constexpr bool SHIFT = FORM == kShift;
   __shared__ float red[2][4 * 32];
   constexpr int kAhead = SHIFT ? 1 : NV == 1 ? 4 : 2;  // combined rows in flight
   constexpr int kGroup = SHIFT && NV == 4 ? 2 : NV;           // vectors of a row in flight
@@ -182,13 +191,13 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : NV == 4 && SHIFT ? 544 : 512)
   pdl_wait();
   pdl_trigger();
   const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
-  const bool live = t < a.T;
+  const bool live = FORM == kFull || t < a.T;
   const int tx = threadIdx.x, nx = blockDim.x, K = a.K;
   T* h = static_cast<T*>(a.h) + t * a.ldh;
   RT* r_out = static_cast<RT*>(a.r_out) + t * a.ldro;
   const int shift = !SHIFT ? 0 : a.h ? row_shift<sizeof(T)>(h) : row_shift<sizeof(RT)>(r_out);
   auto at = [&](int v) { return (v * nx + tx) * 8 - shift; };
-  auto in = [&](int v) { return live && at(v) < K; };
+  auto in = [&](int v) { return FORM == kFull || (live && at(v) < K); };
   float2 b[NV][4];
 #pragma unroll
   for (int v = 0; v < NV; ++v)
@@ -336,14 +345,15 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : NV == 4 && SHIFT ? 544 : 512)
 constexpr float kRoundBias = 12582912.f;
 constexpr float kTiny = 5.4210108624275222e-20f;  // 2^-64; rows below it are scaled by its inverse, so that r is finite
 
-template <typename T, int NV, bool SHIFT>
-__global__ void __launch_bounds__(NV == 1 ? 1024 : NV == 4 && SHIFT ? 544 : 512)
+template <typename T, int NV, int FORM>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : NV == 4 && FORM == kShift ? 544 : 512)
     quantize_rows_kernel(const __grid_constant__ QuantArgs a) {
+  constexpr bool SHIFT = FORM == kShift;
   __shared__ uint32_t red[4 * 32];
   pdl_wait();
   pdl_trigger();
   const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
-  const bool live = row < a.rows;
+  const bool live = FORM == kFull || row < a.rows;
   const int tx = threadIdx.x, nx = blockDim.x, K = a.K;
   const long long s = live ? (a.src ? a.src[row] : row) : -1;
   const bool have = s >= 0 && s < a.x_rows;
@@ -353,7 +363,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : NV == 4 && SHIFT ? 544 : 512)
   Vec8<T, SHIFT> x[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    if (have && at(v) < K) x[v].load(static_cast<const T*>(a.x) + s * a.ldx, at(v), K);
+    if (have && (FORM == kFull || at(v) < K)) x[v].load(static_cast<const T*>(a.x) + s * a.ldx, at(v), K);
     else x[v].zero();
   }
   // the bits of |x| order as |x| does, with NaN above infinity
@@ -377,7 +387,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : NV == 4 && SHIFT ? 544 : 512)
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int e = at(v);
-    if (e >= K) continue;
+    if (FORM != kFull && e >= K) continue;
     float2 f[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = unpack2<T>(w[v][i]);
@@ -422,19 +432,23 @@ RowShape row_shape(long long rows, int nvec, int NV) {
 int row_vectors(int K, bool shift) { return shift ? (K + 14) / 8 : K / 8; }
 
 // Vectors per thread. Few rows: as many threads per row as can be used (a
-// shorter chain). Many rows: fewer, as far as the registers go (less
-// synchronisation per byte): 8192 rows of 4096, one, two or four vectors a
-// thread: norm with two combined rows 98, 65, 68 us; quantiser 28, 21, 18 us.
-// Shifted rows of the norm take one longer: 1027 rows of 2051 9.5 (one), 15 us
-// (two).
+// shorter chain). Many rows: fewer (less synchronisation per byte), as far as
+// the registers leave enough rows on an SM at a time. One, two or four vectors,
+// us: norm with two combined rows, 8192 x 4096 99, 62, 64; 16384 x 1024 43, 30,
+// 31; without, 16384 x 256 7.8, 10.4, 16; quantiser, one or four, 8192 x 4096
+// 27, 16; 16384 x 512 9.4, 6.9; 30000 x 256 8.4, 9.5. Shifted rows of the norm
+// take one longer: 1027 x 2051 9.5, 15.
 int norm_vectors(long long rows, int nvec, bool shift) {
   if (rows <= 2LL * device_sms()) return nvec <= 1024 ? 1 : 4;
-  if (shift) return nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
-  return nvec <= 128 ? 1 : nvec <= 512 ? 2 : 4;
+  return nvec <= (shift ? 512 : 32) ? 1 : nvec <= 1024 ? 2 : 4;
 }
 int quant_vectors(long long rows, int nvec) {
   if (rows <= 2LL * device_sms()) return nvec <= 1024 ? 1 : 4;
-  return nvec <= 128 ? 1 : 4;
+  return nvec < 64 ? 1 : 4;
+}
+
+bool full_rows(const RowShape& s, long long rows, int nvec, int NV) {
+  return rows % s.block.y == 0 && (int)s.block.x * NV == nvec;
 }
 
 template <typename T, typename RT, bool SHIFT>
@@ -442,9 +456,17 @@ cudaError_t norm_typed(const NormArgs& a, cudaStream_t st) {
   const int nvec = row_vectors(a.K, SHIFT), NV = norm_vectors(a.T, nvec, SHIFT);
   const RowShape s = row_shape(a.T, nvec, NV);
   auto go = [&](auto kern) { return launch_kernel(kern, s.grid, s.block, 0, st, true, a); };
-  if (NV == 1) return go(block_norm_kernel<T, RT, 1, SHIFT>);
-  if (NV == 2) return go(block_norm_kernel<T, RT, 2, SHIFT>);
-  return go(block_norm_kernel<T, RT, 4, SHIFT>);
+  constexpr int kBounded = SHIFT ? kShift : kEven;
+  if constexpr (!SHIFT) {
+    if (full_rows(s, a.T, nvec, NV)) {
+      if (NV == 1) return go(block_norm_kernel<T, RT, 1, kFull>);
+      if (NV == 2) return go(block_norm_kernel<T, RT, 2, kFull>);
+      return go(block_norm_kernel<T, RT, 4, kFull>);
+    }
+  }
+  if (NV == 1) return go(block_norm_kernel<T, RT, 1, kBounded>);
+  if (NV == 2) return go(block_norm_kernel<T, RT, 2, kBounded>);
+  return go(block_norm_kernel<T, RT, 4, kBounded>);
 }
 
 template <typename T, bool SHIFT>
@@ -452,8 +474,11 @@ cudaError_t quant_typed(const QuantArgs& a, cudaStream_t st) {
   const int nvec = row_vectors(a.K, SHIFT), NV = quant_vectors(a.rows, nvec);
   const RowShape s = row_shape(a.rows, nvec, NV);
   auto go = [&](auto kern) { return launch_kernel(kern, s.grid, s.block, 0, st, true, a); };
-  if (NV == 1) return go(quantize_rows_kernel<T, 1, SHIFT>);
-  return go(quantize_rows_kernel<T, 4, SHIFT>);
+  constexpr int kBounded = SHIFT ? kShift : kEven;
+  if constexpr (!SHIFT) {
+    if (full_rows(s, a.rows, nvec, NV)) return go(NV == 1 ? quantize_rows_kernel<T, 1, kFull> : quantize_rows_kernel<T, 4, kFull>);
+  }
+  return go(NV == 1 ? quantize_rows_kernel<T, 1, kBounded> : quantize_rows_kernel<T, 4, kBounded>);
 }
 
 }  // namespace
