@@ -320,15 +320,16 @@ def moe_layer_destroy(layer: int) -> None:
 # most of the time): the usual case, a contiguous tensor of the expected shape,
 # is looked at first, outputs made here are not checked, and no views are made.
 
-_DTYPES = {}
+_ENV = None
 
 
-def _dtypes() -> dict:
-    """The library's codes of the torch dtypes."""
-    if not _DTYPES:
+def _env() -> tuple:
+    """(torch, the library, its codes of the torch dtypes), looked up once."""
+    global _ENV
+    if _ENV is None:
         import torch
-        _DTYPES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
-    return _DTYPES
+        _ENV = torch, _lib(), {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+    return _ENV
 
 
 def _require(ok, where: str):
@@ -338,7 +339,7 @@ def _require(ok, where: str):
 
 def _call(index: int, stream, where: str, fn, *args) -> None:
     """fn(*args, stream) with device ``index`` current, on its current stream unless one is given."""
-    import torch
+    torch = _ENV[0]
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(index)
     if index == torch._C._cuda_getDevice():
@@ -348,6 +349,15 @@ def _call(index: int, stream, where: str, fn, *args) -> None:
             status = fn(*args, stream)
     if status != MOE_OK:
         raise MoEError(status, where)
+
+
+def _new(shape, dtype, device, stream):
+    """An output, from the memory pool of the stream that will write it."""
+    torch = _ENV[0]
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device)):
+        return torch.empty(*shape, dtype=dtype, device=device)
 
 
 def _rows(t, where: str, index: int, n, width: int) -> int:
@@ -384,7 +394,7 @@ def moe_block_norm(residual=None, branch=None, *, w_pre=None, w_post=None, gate=
     channel), [T, 1] (per token) or [T, K]. Without w_pre no h is made; without
     a branch no residual_out is made unless one is given. residual_out may be
     ``residual`` itself."""
-    import torch
+    torch, lib, codes = _ENV or _env()
     f = "moe_block_norm"
     lead = residual if residual is not None else branch
     _require(lead is not None and lead.dim() == 2 and lead.is_cuda, f)
@@ -394,20 +404,19 @@ def moe_block_norm(residual=None, branch=None, *, w_pre=None, w_post=None, gate=
         T = inv_pos.shape[0]
     dt = branch.dtype if branch is not None else w_pre.dtype if w_pre is not None else residual.dtype
     rdt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else dt
-    codes = _dtypes()
     a = BlockNormArgs(T, K, codes.get(dt, -1), codes.get(rdt, -1))
     a.residual_scale, a.branch_scale, a.eps, a.weight_offset = residual_scale, branch_scale, eps, weight_offset
     if residual is not None:
         a.residual_stride = _rows(residual, f, index, T, K)
         a.residual = residual.data_ptr()
     # a new output is like the contiguous residual, whose copy costs least
-    like = residual if residual is not None and residual.is_contiguous() else None
+    like = residual if residual is not None and stream is None and residual.is_contiguous() else None
     if residual_out is not None:
         _require(residual_out.dtype is rdt, f)
         a.residual_out_stride = _rows(residual_out, f, index, T, K)
         a.residual_out = residual_out.data_ptr()
     elif branch is not None:
-        residual_out = torch.empty_like(like) if like is not None else torch.empty((T, K), dtype=rdt, device=lead.device)
+        residual_out = torch.empty_like(like) if like is not None else _new((T, K), rdt, lead.device, stream)
         a.residual_out_stride, a.residual_out = K, residual_out.data_ptr()
     if h_out is not None:
         _require(h_out.dtype is dt, f)
@@ -415,7 +424,7 @@ def moe_block_norm(residual=None, branch=None, *, w_pre=None, w_post=None, gate=
         a.h = h_out.data_ptr()
     elif w_pre is not None:
         h_out = (torch.empty_like(like, dtype=dt) if like is not None else
-                 torch.empty((T, K), dtype=dt, device=lead.device))
+                 _new((T, K), dt, lead.device, stream))
         a.h_stride, a.h = K, h_out.data_ptr()
     if branch is not None:
         a.branch_stride = _rows(branch, f, index, T if inv_pos is None else None, K)
@@ -434,21 +443,22 @@ def moe_block_norm(residual=None, branch=None, *, w_pre=None, w_post=None, gate=
             a.gate = _flat(gate, f, index, dt, (K,))
             a.gate_channel_stride = 1
         else:
+            _require(gate.dim() == 2 and gate.dtype is dt, f)
             width = gate.shape[1]
-            _require(gate.dtype is dt and (width == 1 or width == K), f)
+            _require(width == 1 or width == K, f)
             a.gate_token_stride = _rows(gate, f, index, T, width)
             a.gate_channel_stride = 0 if width == 1 else 1
             a.gate = gate.data_ptr()
         a.gate_sigmoid = 1 if gate_sigmoid else 0
     if T > 0:
-        _call(index, stream, f, _lib().moe_block_norm, ctypes.byref(a))
+        _call(index, stream, f, lib.moe_block_norm, ctypes.byref(a))
     return residual_out, h_out
 
 
 def moe_quantize_rows(x, src_rows=None, codes=None, scales=None, stream: Optional[int] = None):
     """Rows of x (bf16 or fp16 [M, K]), or the rows src_rows (int32 [R]) selects,
     as 8-bit codes with one scale each; returns (codes int8 [R, K], scales fp32 [R])."""
-    import torch
+    torch, lib, dtypes = _ENV or _env()
     f = "moe_quantize_rows"
     _require(x.dim() == 2 and x.is_cuda, f)
     index = x.get_device()
@@ -460,23 +470,23 @@ def moe_quantize_rows(x, src_rows=None, codes=None, scales=None, stream: Optiona
         R = src_rows.shape[0]
         src = _flat(src_rows, f, index, torch.int32, (R,))
     if codes is None:
-        codes, ldq = torch.empty(R, K, dtype=torch.int8, device=x.device), K
+        codes, ldq = _new((R, K), torch.int8, x.device, stream), K
     else:
         _require(codes.dtype is torch.int8, f)
         ldq = _rows(codes, f, index, R, K)
     if scales is None:
-        scales = torch.empty(R, dtype=torch.float32, device=x.device)
+        scales = _new((R,), torch.float32, x.device, stream)
         sp = scales.data_ptr()
     else:
         sp = _flat(scales, f, index, torch.float32, (R,))
-    _call(index, stream, f, _lib().moe_quantize_rows, x.data_ptr(), ldx, M, _dtypes().get(x.dtype, -1), src, R, K,
+    _call(index, stream, f, lib.moe_quantize_rows, x.data_ptr(), ldx, M, dtypes.get(x.dtype, -1), src, R, K,
           codes.data_ptr(), ldq, sp)
     return codes, scales
 
 
-def _product(f, x, w, offsets, out_dtype, out):
+def _product(f, x, w, offsets, out_dtype, out, stream):
     """Checks of the grouped products and their common arguments."""
-    import torch
+    torch = _ENV[0]
     if x.dim() != 2 or not x.is_cuda or w.dtype is not x.dtype or w.get_device() != x.get_device():
         raise MoEError(1, f)
     index = x.get_device()
@@ -495,7 +505,7 @@ def _product(f, x, w, offsets, out_dtype, out):
     if offsets is not None:
         off = _flat(offsets, f, index, torch.int32, (E + 1,))
     if out is None:
-        out, ldy = torch.empty(R, N, dtype=out_dtype, device=x.device), N
+        out, ldy = _new((R, N), out_dtype, x.device, stream), N
     else:
         _require(out_dtype is None or out.dtype is out_dtype, f)
         ldy = _rows(out, f, index, R, N)
@@ -509,16 +519,16 @@ def moe_int8_matmul(x, row_scales, w, channel_scales, offsets=None, out_dtype=No
     [E, N]), e the expert whose range offsets[e] <= r < offsets[e + 1] holds r
     (int32 [E + 1] on the device; None: one matrix for all rows). Rows in no
     range are left as they were. out_dtype: bf16 (default), fp16 or fp32."""
-    import torch
+    torch, lib, codes = _ENV or _env()
     f = "moe_int8_matmul"
     _require(x.dtype is torch.int8, f)
     if out is None and out_dtype is None:
         out_dtype = torch.bfloat16
-    index, ldx, ldw, ldwe, off, R, E, K, N, out, ldy = _product(f, x, w, offsets, out_dtype, out)
+    index, ldx, ldw, ldwe, off, R, E, K, N, out, ldy = _product(f, x, w, offsets, out_dtype, out, stream)
     xs = _flat(row_scales, f, index, torch.float32, (R,))
     ws = _flat(channel_scales, f, index, torch.float32, w.shape[:-1])
-    _call(index, stream, f, _lib().moe_int8_matmul, x.data_ptr(), ldx, xs, w.data_ptr(), ldw, ldwe, ws, off, R, E, K, N,
-          out.data_ptr(), ldy, _dtypes().get(out.dtype, -1))
+    _call(index, stream, f, lib.moe_int8_matmul, x.data_ptr(), ldx, xs, w.data_ptr(), ldw, ldwe, ws, off, R, E, K, N,
+          out.data_ptr(), ldy, codes.get(out.dtype, -1))
     return out
 
 
@@ -526,12 +536,12 @@ def moe_grouped_matmul(x, w, offsets=None, out_dtype=None, out=None, stream: Opt
     """y[r, n] = sum_k x[r, k] w[e, n, k] of bf16 or fp16 rows x [R, K] in expert
     order and experts w [E, N, K] (or [N, K]); offsets as for moe_int8_matmul.
     out_dtype: bf16, fp16 or fp32 (default: x's)."""
+    _, lib, codes = _ENV or _env()
     f = "moe_grouped_matmul"
     if out is None and out_dtype is None:
         out_dtype = x.dtype
-    index, ldx, ldw, ldwe, off, R, E, K, N, out, ldy = _product(f, x, w, offsets, out_dtype, out)
-    codes = _dtypes()
-    _call(index, stream, f, _lib().moe_grouped_matmul, x.data_ptr(), ldx, w.data_ptr(), ldw, ldwe, off, R, E, K, N,
+    index, ldx, ldw, ldwe, off, R, E, K, N, out, ldy = _product(f, x, w, offsets, out_dtype, out, stream)
+    _call(index, stream, f, lib.moe_grouped_matmul, x.data_ptr(), ldx, w.data_ptr(), ldw, ldwe, off, R, E, K, N,
           codes.get(x.dtype, -1), out.data_ptr(), ldy, codes.get(out.dtype, -1))
     return out
 

@@ -145,6 +145,30 @@ def test_block_norm(bq, T, K, dtype, res, opt):
         check(got_h, h, tol_h + half_step(DT[dtype], h), "h")
 
 
+@pytest.mark.parametrize("T,K,dtype,res,opt", [
+    (300, 4096, "bf16", "bf16", dict(k=2, gate="channel", drop=True)),
+    (301, 2048, "fp16", "fp32", dict(gate="token", sig=True)),
+    (310, 256, "bf16", "fp32", {}),
+    (304, 512, "bf16", "bf16", dict(k=3, gate="element")),
+    (303, 512, "fp16", "fp16", dict(gate="element", sig=True)),
+    (299, 1000, "bf16", "bf16", dict(k=2)),
+    (297, 7000, "bf16", "fp32", dict(k=6, gate="token", drop=True)),
+    (297, 8192, "fp16", "fp16", dict(k=1)),
+    (298, 14336, "bf16", "fp32", dict(k=2, gate="channel")),
+    (298, 8200, "fp16", "fp16", dict(gate="element")),
+    (300, 97, "bf16", "bf16", dict(k=2, gate="element")),
+    (297, 2051, "fp16", "fp32", dict(k=2, gate="channel", drop=True)),
+    (297, 6001, "bf16", "bf16", dict(k=8, gate="element", sig=True)),
+    (297, 9001, "fp16", "fp16", dict(k=2, gate="element")),
+    (297, 8999, "bf16", "fp32", dict(pad=2, gate="channel")),
+    (297, 4100, "bf16", "bf16", dict(post=False, pad=3, shift=5)),
+    (30, 9001, "bf16", "bf16", dict(k=2, shift=3, pad=4)),
+])
+def test_block_norm_row_shapes(bq, T, K, dtype, res, opt):
+    """More rows than run at one time, and every way in which rows may lie."""
+    test_block_norm(bq, T, K, dtype, res, opt)
+
+
 def test_block_norm_forms(bq):
     """Plain pre-norm, no residual, in place, outputs into strided views, and rows of zeros."""
     y, r, kw = norm_case(bq, 5, 256, "bf16", "bf16")
@@ -214,6 +238,36 @@ def test_quantize_rows(bq, M, K, dtype, gather, pad):
     want_q, want_s = orc.quantize_rows(f64(x), None if src is None else src.cpu().numpy())
     assert np.array_equal(q.cpu().numpy(), want_q)
     assert np.array_equal(s.cpu().numpy(), want_s.astype(np.float32))
+
+
+@pytest.mark.parametrize("M,K,dtype,gather,pad", [
+    (300, 4096, "bf16", False, 0), (301, 14336, "fp16", True, 0), (297, 512, "bf16", True, 0), (300, 4104, "fp16", False, 8),
+    (298, 9001, "bf16", False, 0), (310, 16383, "fp16", False, 1), (400, 255, "bf16", True, 2), (303, 1024, "fp16", False, 3),
+])
+def test_quantize_row_shapes(bq, M, K, dtype, gather, pad):
+    test_quantize_rows(bq, M, K, dtype, gather, pad)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_quantize_rows_ties(bq, dtype):
+    """Rows of every finite magnitude up to their largest one, whose odd part is
+    small, so that many quotients are half-integers; and scales near both ends of
+    the type's range."""
+    dt = DT[dtype]
+    values = torch.arange(0x7c00 if dtype == "fp16" else 0x7f80, dtype=torch.int16).view(dt).double()
+    lowest = float(values[1])
+    tops = [lowest * m for m in (1, 3, 127, 254, 255, 1000)] + [m * 2.0 ** e for m in (1, 1.5, 1.25, 1.875, 127 / 64, 127 / 128 + 1)
+                                                            for e in (-10, 0, 5)] + [float(values[-1]), float(values[-2])]
+    if dtype == "bf16":
+        tops += [1.5 * 2.0 ** e for e in (-126, -120, -65, -64, -63, 64, 127)]
+    for top in tops:
+        top = float(torch.tensor(top, dtype=torch.float64).to(dt).double())
+        below = values[(values <= top) & (values > top / 300)]
+        row = torch.cat([below[-8000:], -below[-8000:], torch.tensor([top, 0.0], dtype=torch.float64)])
+        q, s = bq.moe_quantize_rows(row.to(dt).cuda()[None])
+        want_q, want_s = orc.quantize_rows(row.numpy()[None])
+        assert np.array_equal(q.cpu().numpy(), want_q), top
+        assert np.array_equal(s.cpu().numpy(), want_s.astype(np.float32)), top
 
 
 def test_quantize_rows_extremes(bq):
@@ -300,6 +354,40 @@ def run_exact(bq, op, out, counts, N, K, lead=0, tail=0, pad=0, shift=0, dense=F
 ])
 def test_products_exact(bq, op, counts, N, K, opt):
     run_exact(bq, op, "fp32", counts, N, K, **opt)
+
+
+@pytest.mark.parametrize("op", ["bf16", "int8"])
+@pytest.mark.parametrize("counts,N,K,opt", [
+    ([1], 2816, 2048, dict(dense=True)),
+    ([16], 512, 4096, dict(dense=True)),
+    ([17], 1024, 8192, dict(dense=True)),
+    ([100], 640, 2048, dict(dense=True)),
+    ([128], 1024, 4096, dict(dense=True)),
+    ([250], 4096, 512, dict(dense=True)),
+    ([500], 4000, 256, dict(dense=True)),
+    ([760], 4096, 128, dict(dense=True)),
+    ([1290], 4096, 64, dict(dense=True)),
+    ([2100], 1500, 64, dict(dense=True)),
+    ([90, 1, 0, 2, 3], 256, 2048, dict(lead=1, tail=2)),
+    ([1, 1, 1, 77], 512, 4096, {}),
+    ([33, 15, 16, 17, 0, 49], 128, 1024, {}),
+    ([900, 0, 5, 3], 1100, 128, dict(tail=3)),
+    ([64] * 9, 384, 640, {}),
+])
+def test_products_tile_forms(bq, op, counts, N, K, opt):
+    """Sizes over the range in which the tiles' width and the split of K change."""
+    run_exact(bq, op, "fp32", counts, N, K, **opt)
+    run_exact(bq, op, "bf16", counts, N, K, **opt)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_products_random_shapes(bq, seed):
+    rng = np.random.default_rng(100 + seed)
+    E = int(rng.choice([1, 2, 7, 32]))
+    counts = (rng.integers(0, 3, E) * np.exp(rng.uniform(0, 5, E))).astype(int).tolist()
+    op = ["bf16", "fp16", "int8"][seed % 3]
+    N, K = int(np.exp(rng.uniform(3, 7))), int(np.exp(rng.uniform(3, 7.5))) // 16 * 16 + 16
+    run_exact(bq, op, "fp32", counts, N, K, lead=int(rng.integers(0, 3)), tail=int(rng.integers(1, 4)))
 
 
 @pytest.mark.parametrize("op,out", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "fp16"), ("int8", "bf16"),
@@ -463,6 +551,19 @@ def test_refusals_on_the_device(bq):
     assert bq.moe_op_sync_status() == 0
 
 
+def test_block_norm_refused_forms(bq):
+    x = torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
+    for kw in (dict(gate=torch.ones(8, 1, 64, dtype=torch.bfloat16, device="cuda")),
+               dict(gate=torch.ones((), dtype=torch.bfloat16, device="cuda")),
+               dict(gate=torch.ones(1, 64, dtype=torch.bfloat16, device="cuda")),
+               dict(h_out=torch.zeros_like(x)),
+               dict(residual_out=x[:, :32]),
+               dict(residual_out=x.expand(8, 64).float())):
+        with pytest.raises(bq.MoEError) as ei:
+            bq.moe_block_norm(x, x, **kw)
+        assert ei.value.status == 1
+
+
 # ---------------------------------------------------------------------------
 # streams, graphs and the calls together
 # ---------------------------------------------------------------------------
@@ -560,6 +661,30 @@ def test_operators_on_other_streams(bq):
     torch.cuda.synchronize()
     for i, g in enumerate(got):
         assert torch.equal(g[0], want[i % 2][0]) and torch.equal(g[1], want[i % 2][1])
+
+
+def test_operators_on_a_given_stream(bq):
+    """Outputs made for a call on another stream belong to that stream: freed and
+    asked for again on the current one they do not come back while it may write."""
+    s = chain_state(bq, 200, 8, 2, 256, 128, 6)
+    (want_r, want_h), (h, gu, z, o) = chain(bq, s)
+    want_q, want_qs = bq.moe_quantize_rows(h, s["perm"])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    st = side.cuda_stream
+    for _ in range(3):
+        _, h1 = bq.moe_block_norm(s["res"], w_pre=s["w1n"], stream=st)
+        q, qs = bq.moe_quantize_rows(h1, s["perm"], stream=st)
+        gu1 = bq.moe_int8_matmul(q, qs, s["w1q"], s["w1s"], s["off"], out_dtype=torch.float32, stream=st)
+        o1 = bq.moe_grouped_matmul(z, s["w2"], s["off"], stream=st)
+        r, hh = bq.moe_block_norm(s["res"], o1, w_post=s["w2n"], w_pre=s["w3n"], branch_scale=0.5, inv_pos=s["inv"],
+                                  pair_weights=s["pw"], stream=st)
+        del h1
+        scratch = torch.full_like(h, 9.0)
+        torch.cuda.synchronize()
+        assert torch.equal(q, want_q) and torch.equal(qs, want_qs) and torch.equal(gu1, gu) and torch.equal(o1, o)
+        assert torch.equal(r, want_r) and torch.equal(hh, want_h) and bool((scratch == 9.0).all())
+    assert bq.moe_op_sync_status(st) == 0
 
 
 def test_operators_captured(bq):
