@@ -48,7 +48,7 @@ constexpr int kStagingBytes = kEpiWarps * 2048;
 
 struct TcArgs {
   CUtensorMap map_w;   // [E][N][K], box 128 rows
-  CUtensorMap map_x[4];  // [rows][K], boxes of 32, 64, 96 and 128 rows: one copy per stage
+  CUtensorMap map_x[4];  // [rows][K], boxes of 32, 64, 96 and 128 rows as far as nmax needs them: one copy per stage
   GroupedArgs g;
   uint32_t idesc;      // without the N field
   int NF;              // channel tiles
@@ -345,7 +345,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
   if (warp == 0 && elect_one()) {
     prefetch_map(&a.map_w);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) prefetch_map(&a.map_x[b]);
+    for (int b = 0; b < 4; ++b)
+      if (b * kBoxRows * CG < a.nmax) prefetch_map(&a.map_x[b]);
   }
   if (warp == 1) alloc_tmem<CG>(smem_u32(&tmem_slot), kCols);
   tc_fence_before();
@@ -664,8 +665,6 @@ cudaError_t launch_grouped_tc(const GroupedArgs& g, int op, int y_dtype, cudaStr
   const long long ldx = g.rows > 1 ? g.ldx : (g.K + 15) / 16 * 16;
   const long long ldwe = g.E > 1 ? g.ldwe : g.ldw * g.N;
   if (!encode_rows(&a.map_w, g.w, op, es, g.K, g.N, g.ldw, g.E, ldwe, 128)) return cudaErrorInvalidValue;
-  for (int b = 0; b < 4; ++b)
-    if (!encode_rows(&a.map_x[b], g.x, op, es, g.K, g.rows, ldx, 0, 0, (b + 1) * kBoxRows)) return cudaErrorInvalidValue;
   a.vec = reinterpret_cast<uintptr_t>(g.y) % 8 == 0 && g.ldy % 4 == 0;
   a.idesc = op == kOpInt8 ? (2u << 4) | (1u << 7) | (1u << 10)
                           : (1u << 4) | ((op == DT_BF16 ? 1u : 0u) << 7) | ((op == DT_BF16 ? 1u : 0u) << 10);
@@ -678,21 +677,20 @@ cudaError_t launch_grouped_tc(const GroupedArgs& g, int op, int y_dtype, cudaStr
   // nearly as much as wide ones, and it is the number of tiles that a CTA works
   // off one after the other that counts. The split of K (CG = 1) pays an
   // exchange of the partial sums, about 3500 cycles and 40 a column.
-  const long long groups = std::min<long long>(g.rows, g.E);
-  const long long mean = (g.rows + groups - 1) / groups;
-  const long long streamed = groups * g.N * nk * kRowBytes / 3500;  // weights at HBM's bytes per cycle
-  auto tiles_of = [&](int cg, int width) { return groups * ((mean + width - 1) / width) * ((g.N + 128 * cg - 1) / (128 * cg)); };
+  const int groups = std::min(g.rows, g.E), mean = (g.rows - 1) / groups + 1;
+  const int nf[3] = {0, (g.N - 1) / 128 + 1, (g.N - 1) / 256 + 1};  // channel tiles by CG
+  const double streamed = (double)groups * g.N * nk * (kRowBytes / 3500.0);  // weights at HBM's bytes per cycle
   auto cost_of = [&](int cg, int width, int S) {
-    const long long nt = (mean + width - 1) / width, unit = cg == 2 || S == 8 ? 32 : 16;
-    const long long n = ((mean + nt - 1) / nt + unit - 1) / unit * unit;
-    const long long per_k = std::max(2 * n, (128 + n / cg) * kRowBytes / 55);
-    const long long slots = cg == 2 ? pairs : sms / S, waves = (tiles_of(cg, width) + slots - 1) / slots;
-    return std::max(waves * ((nk + S - 1) / S) * per_k, streamed) + (S > 1 ? 3500 + 40 * n : 0);
+    const int nt = (mean - 1) / width + 1, unit = cg == 2 || S == 8 ? 32 : 16;
+    const int n = ((mean - 1) / nt / unit + 1) * unit;
+    const int waves = (groups * nt * nf[cg] - 1) / (cg == 2 ? pairs : sms / S) + 1;
+    const double per_k = std::max(2.0 * n, (128 + n / cg) * (kRowBytes / 55.0));
+    return std::max(waves * per_k * ((nk - 1) / S + 1), streamed) + (S > 1 ? 3500 + 40 * n : 0);
   };
   int cg = 2, width = 256, S = 1;
-  long long best = cost_of(2, 256, 1);
+  double best = cost_of(2, 256, 1);
   auto consider = [&](int c, int w, int s) {
-    const long long cost = cost_of(c, w, s);
+    const double cost = cost_of(c, w, s);
     if (cost < best) {
       best = cost;
       cg = c;
@@ -700,15 +698,16 @@ cudaError_t launch_grouped_tc(const GroupedArgs& g, int op, int y_dtype, cudaStr
       S = s;
     }
   };
-  for (int w = 224; w >= 64; w -= 32) consider(2, w, 1);
+  for (int w = 224; w >= 64; w -= 32)
+    if (mean > w - 32) consider(2, w, 1);  // a narrower tile holds the rest
   // few tiles: single CTAs, split along K while there are CTAs for it
   for (int w = 128; w >= 16; w /= 2) {
     if (mean <= w / 2 && w > 16) continue;
-    const long long tiles = groups * ((g.N + 127) / 128) * ((mean + w - 1) / w);
+    const int tiles = groups * nf[1] * ((mean - 1) / w + 1);
     for (int s = 1; s <= 8 && tiles * s <= sms; s *= 2)
       if (s == 1 || nk >= s * 2) consider(1, w, s);
   }
-  a.NF = (g.N + 128 * cg - 1) / (128 * cg);
+  a.NF = nf[cg];
   a.nf_inv = (uint32_t)((1ull << 32) / a.NF + 1);
   a.unit = cg == 2 || S == 8 ? 32 : 16;
   a.nmax = std::max(width, a.unit);
@@ -716,7 +715,9 @@ cudaError_t launch_grouped_tc(const GroupedArgs& g, int op, int y_dtype, cudaStr
   a.idesc |= (uint32_t)(128 * cg >> 4) << 24;
   // ceil(r / n) summed over the groups' rows r: at most one tile for each of
   // them and one for every n of the other rows
-  const long long most = (groups + (g.rows - groups) / a.nmax) * a.NF;
+  const long long most = (long long)(groups + (g.rows - groups) / a.nmax) * a.NF;
+  for (int b = 0; b < 4 && b * kBoxRows * cg < a.nmax; ++b)
+    if (!encode_rows(&a.map_x[b], g.x, op, es, g.K, g.rows, ldx, 0, 0, (b + 1) * kBoxRows)) return cudaErrorInvalidValue;
   if (cg == 2) {
     a.bslot = 128 * kRowBytes;
     a.stages = 6;
