@@ -25,6 +25,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kernels.h"
 #include "ops.cuh"
@@ -293,6 +294,8 @@ __device__ __forceinline__ void store_chunk(const TcArgs& a, const Tile& t, int 
     }
   }
 }
+
+#include "grouped_loads.cuh"
 
 template <int CG, bool I8, typename TO>
 __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_constant__ TcArgs a) {
@@ -602,17 +605,24 @@ bool encode_rows(CUtensorMap* m, const void* base, int op, int es, long long K, 
 
 constexpr int kSmemBudget = 221 * 1024;  // dynamic; the static tables take about 6 KiB more
 
-template <int CG, bool I8, typename TO>
-cudaError_t launch_tc(const TcArgs& a, int clusters, size_t smem, cudaStream_t st) {
-  static std::atomic<unsigned long long> set{0};  // devices whose attribute is set
+// Raises a kernel's limit of dynamic shared memory once per device; set holds
+// the devices done.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<unsigned long long>& set) {
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
-  if (dev > 63 || !(set.load(std::memory_order_acquire) >> dev & 1)) {
-    err = cudaFuncSetAttribute(grouped_tc_kernel<CG, I8, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget);
-    if (err != cudaSuccess) return err;
-    if (dev <= 63) set.fetch_or(1ull << dev, std::memory_order_release);
-  }
+  if (dev <= 63 && (set.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == cudaSuccess && dev <= 63) set.fetch_or(1ull << dev, std::memory_order_release);
+  return err;
+}
+
+template <int CG, bool I8, typename TO>
+cudaError_t launch_tc(const TcArgs& a, int clusters, size_t smem, cudaStream_t st) {
+  static std::atomic<unsigned long long> set{0};
+  const cudaError_t err = allow_smem(grouped_tc_kernel<CG, I8, TO>, kSmemBudget, set);
+  if (err != cudaSuccess) return err;
   const int csize = CG == 2 ? 2 : a.S;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(clusters * csize);
@@ -629,16 +639,51 @@ cudaError_t launch_tc(const TcArgs& a, int clusters, size_t smem, cudaStream_t s
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, I8, TO>, a);
 }
+template <bool I8, typename TO>
+cudaError_t launch_loads(const TcArgs& a, int grid, cudaStream_t st) {
+  constexpr int kSmem = kStagesLoads * (kABytes + 128 * kRowBytes) + 1024;
+  static std::atomic<unsigned long long> set{0};
+  const cudaError_t err = allow_smem(grouped_loads_kernel<I8, TO>, kSmem, set);
+  if (err != cudaSuccess) return err;
+  return launch_kernel(grouped_loads_kernel<I8, TO>, dim3(grid), dim3(kThreadsLoads), kSmem, st, true, a);
+}
+// go(whether the operands are 8-bit, a value of the output type)
+template <typename Go>
+cudaError_t by_types(int op, int y_dtype, Go go) {
+  auto by_out = [&](auto i8) {
+    if (y_dtype == DT_BF16) return go(i8, __nv_bfloat16{});
+    if (y_dtype == DT_FP16) return go(i8, __half{});
+    return go(i8, 0.f);
+  };
+  return op == kOpInt8 ? by_out(std::true_type{}) : by_out(std::false_type{});
+}
 template <int CG>
 cudaError_t launch_tc_typed(const TcArgs& a, int op, int y_dtype, int clusters, size_t smem, cudaStream_t st) {
-  if (op == kOpInt8) {
-    if (y_dtype == DT_BF16) return launch_tc<CG, true, __nv_bfloat16>(a, clusters, smem, st);
-    if (y_dtype == DT_FP16) return launch_tc<CG, true, __half>(a, clusters, smem, st);
-    return launch_tc<CG, true, float>(a, clusters, smem, st);
-  }
-  if (y_dtype == DT_BF16) return launch_tc<CG, false, __nv_bfloat16>(a, clusters, smem, st);
-  if (y_dtype == DT_FP16) return launch_tc<CG, false, __half>(a, clusters, smem, st);
-  return launch_tc<CG, false, float>(a, clusters, smem, st);
+  return by_types(op, y_dtype, [&](auto i8, auto out) {
+    return launch_tc<CG, decltype(i8)::value, decltype(out)>(a, clusters, smem, st);
+  });
+}
+
+// what every form of the kernels needs; the instruction descriptor without its N field
+TcArgs common_args(const GroupedArgs& g, int op, int cg, int width, int unit) {
+  TcArgs a{};
+  a.g = g;
+  a.vec = reinterpret_cast<uintptr_t>(g.y) % 8 == 0 && g.ldy % 4 == 0;
+  a.idesc = op == kOpInt8 ? (2u << 4) | (1u << 7) | (1u << 10)
+                          : (1u << 4) | ((op == DT_BF16 ? 1u : 0u) << 7) | ((op == DT_BF16 ? 1u : 0u) << 10);
+  a.idesc |= (uint32_t)(128 * cg >> 4) << 24;
+  a.NF = (g.N - 1) / (128 * cg) + 1;
+  a.nf_inv = (uint32_t)((1ull << 32) / a.NF + 1);
+  a.unit = unit;
+  a.nmax = std::max(width, unit);
+  a.S = 1;
+  return a;
+}
+// ceil(r / n) summed over the groups' rows r is at most one tile for each group
+// that can have rows and one for every n of the other rows
+long long most_tiles(const GroupedArgs& g, int width, int NF) {
+  const int groups = std::min(g.rows, g.E);
+  return (long long)(groups + (g.rows - groups) / width) * NF;
 }
 
 }  // namespace
@@ -660,14 +705,8 @@ bool grouped_tc_fits(const GroupedArgs& a, int op) {
 cudaError_t launch_grouped_tc(const GroupedArgs& g, int op, int y_dtype, cudaStream_t st) {
   const int es = op == kOpInt8 ? 1 : 2;
   const int sms = device_sms(), pairs = sms / 2;
-  TcArgs a{};
-  a.g = g;
   const long long ldx = g.rows > 1 ? g.ldx : (g.K + 15) / 16 * 16;
   const long long ldwe = g.E > 1 ? g.ldwe : g.ldw * g.N;
-  if (!encode_rows(&a.map_w, g.w, op, es, g.K, g.N, g.ldw, g.E, ldwe, 128)) return cudaErrorInvalidValue;
-  a.vec = reinterpret_cast<uintptr_t>(g.y) % 8 == 0 && g.ldy % 4 == 0;
-  a.idesc = op == kOpInt8 ? (2u << 4) | (1u << 7) | (1u << 10)
-                          : (1u << 4) | ((op == DT_BF16 ? 1u : 0u) << 7) | ((op == DT_BF16 ? 1u : 0u) << 10);
   const int nk = (g.K * es + kRowBytes - 1) / kRowBytes;
   // Tile width and form. Groups are taken as equally large (their sizes are
   // only known on the device). What a tile takes per 128 bytes of K is the
@@ -707,15 +746,10 @@ cudaError_t launch_grouped_tc(const GroupedArgs& g, int op, int y_dtype, cudaStr
     for (int s = 1; s <= 8 && tiles * s <= sms; s *= 2)
       if (s == 1 || nk >= s * 2) consider(1, w, s);
   }
-  a.NF = nf[cg];
-  a.nf_inv = (uint32_t)((1ull << 32) / a.NF + 1);
-  a.unit = cg == 2 || S == 8 ? 32 : 16;
-  a.nmax = std::max(width, a.unit);
+  TcArgs a = common_args(g, op, cg, width, cg == 2 || S == 8 ? 32 : 16);
   a.S = S;
-  a.idesc |= (uint32_t)(128 * cg >> 4) << 24;
-  // ceil(r / n) summed over the groups' rows r: at most one tile for each of
-  // them and one for every n of the other rows
-  const long long most = (long long)(groups + (g.rows - groups) / a.nmax) * a.NF;
+  const long long most = most_tiles(g, a.nmax, a.NF);
+  if (!encode_rows(&a.map_w, g.w, op, es, g.K, g.N, g.ldw, g.E, ldwe, 128)) return cudaErrorInvalidValue;
   for (int b = 0; b < 4 && b * kBoxRows * cg < a.nmax; ++b)
     if (!encode_rows(&a.map_x[b], g.x, op, es, g.K, g.rows, ldx, 0, 0, (b + 1) * kBoxRows)) return cudaErrorInvalidValue;
   if (cg == 2) {
@@ -730,6 +764,17 @@ cudaError_t launch_grouped_tc(const GroupedArgs& g, int op, int y_dtype, cudaStr
   const size_t smem = (size_t)a.stages * (kABytes + a.bslot) + fixed;
   const int clusters = (int)(a.S > 1 ? most : std::min<long long>(most, sms));
   return launch_tc_typed<1>(a, op, y_dtype, clusters, smem, st);
+}
+
+cudaError_t launch_grouped_loads(const GroupedArgs& g, int op, int y_dtype, cudaStream_t st) {
+  const int NF = (g.N - 1) / 128 + 1;
+  int width = 128;  // narrower only where there would not be a tile for every SM
+  while (width > 16 && most_tiles(g, width, NF) < device_sms()) width /= 2;
+  const TcArgs a = common_args(g, op, 1, width, 16);
+  const int grid = (int)std::min<long long>(most_tiles(g, width, NF), 2LL * device_sms());
+  return by_types(op, y_dtype, [&](auto i8, auto out) {
+    return launch_loads<decltype(i8)::value, decltype(out)>(a, grid, st);
+  });
 }
 
 cudaError_t read_op_status(unsigned* out, cudaStream_t st) {

@@ -15,23 +15,28 @@ std::atomic<unsigned long long> g_wait_ns{kDefaultWaitNs};
 bool is16(int d) { return d == MOE_BF16 || d == MOE_FP16; }
 bool is_out(int d) { return is16(d) || d == MOE_FP32; }
 
+// whether a pointer lies at a multiple of its elements' size
+bool at_elements(const void* p, int es) { return reinterpret_cast<uintptr_t>(p) % es == 0; }
+
 moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 // checks shared by the two products
 moe_status_t check_product(const void* x, long long ldx, const void* w, long long ldw, long long ldwe,
-                           const int* offsets, int rows, int E, int K, int N, const void* y, long long ldy, int yd) {
+                           int es, const int* offsets, int rows, int E, int K, int N, const void* y, long long ldy,
+                           int yd) {
   if (rows < 0 || E < 1 || K < 1 || N < 1 || !is_out(yd)) return MOE_ERR_INVALID_ARG;
   if (E > kMaxExperts) return MOE_ERR_TOO_LARGE;
   if (!offsets && E != 1) return MOE_ERR_INVALID_ARG;
   if (ldx < 0 || ldw < 0 || ldwe < 0 || (rows > 1 && ldy < N)) return MOE_ERR_INVALID_ARG;
   if (rows > 0 && (!x || !w || !y)) return MOE_ERR_INVALID_ARG;
+  if (!at_elements(x, es) || !at_elements(w, es) || !at_elements(y, yd == MOE_FP32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
 moe_status_t run_product(GroupedArgs& a, int op, int y_dtype, cudaStream_t st) {
   a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   return cuda_status(grouped_tc_fits(a, op) ? launch_grouped_tc(a, op, y_dtype, st)
-                                            : launch_grouped_plain(a, op, y_dtype, st));
+                                            : launch_grouped_loads(a, op, y_dtype, st));
 }
 
 }  // namespace
@@ -56,6 +61,11 @@ moe_status_t moe_block_norm(const moe_block_norm_t* p, void* cuda_stream) {
     return MOE_ERR_INVALID_ARG;
   if (!(p->eps >= 0.f) || !std::isfinite(p->eps) || !std::isfinite(p->weight_offset) ||
       !std::isfinite(p->residual_scale) || !std::isfinite(p->branch_scale))
+    return MOE_ERR_INVALID_ARG;
+  const int rs = p->residual_dtype == MOE_FP32 ? 4 : 2;
+  if (!at_elements(p->branch, 2) || !at_elements(p->post_weight, 2) || !at_elements(p->gate, 2) ||
+      !at_elements(p->pre_weight, 2) || !at_elements(p->h, 2) || !at_elements(p->residual, rs) ||
+      !at_elements(p->residual_out, rs))
     return MOE_ERR_INVALID_ARG;
   if (p->tokens == 0) return MOE_OK;
   NormArgs a{};
@@ -95,6 +105,7 @@ moe_status_t moe_quantize_rows(const void* x, long long x_stride, int x_rows, mo
     return MOE_ERR_INVALID_ARG;
   if (width > kMaxRowWidth) return MOE_ERR_TOO_LARGE;
   if (rows > 0 && ((!x && x_rows > 0) || !codes || !scales)) return MOE_ERR_INVALID_ARG;
+  if (!at_elements(x, 2)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
   QuantArgs a{x, x_stride, x_rows, src_rows, rows, width, codes, codes_stride, scales};
   return cuda_status(launch_quantize_rows(a, dtype, static_cast<cudaStream_t>(cuda_stream)));
@@ -104,7 +115,7 @@ moe_status_t moe_int8_matmul(const signed char* x, long long x_stride, const flo
                              long long w_stride, long long expert_stride, const float* channel_scales,
                              const int* offsets, int rows, int experts, int K, int N, void* y, long long y_stride,
                              moe_dtype_t y_dtype, void* cuda_stream) {
-  const moe_status_t s = check_product(x, x_stride, w, w_stride, expert_stride, offsets, rows, experts, K, N, y,
+  const moe_status_t s = check_product(x, x_stride, w, w_stride, expert_stride, 1, offsets, rows, experts, K, N, y,
                                        y_stride, y_dtype);
   if (s != MOE_OK) return s;
   if (K > 131071) return MOE_ERR_TOO_LARGE;
@@ -120,7 +131,7 @@ moe_status_t moe_grouped_matmul(const void* x, long long x_stride, const void* w
                                 moe_dtype_t dtype, void* y, long long y_stride, moe_dtype_t y_dtype,
                                 void* cuda_stream) {
   if (!is16(dtype)) return MOE_ERR_INVALID_ARG;
-  const moe_status_t s = check_product(x, x_stride, w, w_stride, expert_stride, offsets, rows, experts, K, N, y,
+  const moe_status_t s = check_product(x, x_stride, w, w_stride, expert_stride, 2, offsets, rows, experts, K, N, y,
                                        y_stride, y_dtype);
   if (s != MOE_OK) return s;
   if (rows == 0) return MOE_OK;

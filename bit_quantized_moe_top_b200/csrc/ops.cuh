@@ -63,9 +63,10 @@ cudaError_t launch_block_norm(const NormArgs& a, int dtype, int res_dtype, cudaS
 cudaError_t launch_quantize_rows(const QuantArgs& a, int dtype, cudaStream_t st);
 // operand type: DT_BF16, DT_FP16, or kOpInt8
 constexpr int kOpInt8 = 3;
-cudaError_t launch_grouped_plain(const GroupedArgs& a, int op, int y_dtype, cudaStream_t st);
 bool grouped_tc_fits(const GroupedArgs& a, int op);
 cudaError_t launch_grouped_tc(const GroupedArgs& a, int op, int y_dtype, cudaStream_t st);
+// for the calls that do not fit
+cudaError_t launch_grouped_loads(const GroupedArgs& a, int op, int y_dtype, cudaStream_t st);
 // the products' device status word, read and cleared once the stream is idle
 cudaError_t read_op_status(unsigned* out, cudaStream_t st);
 

@@ -150,3 +150,15 @@ def test_oracle_grouped_brute_force():
     for r, e in ((1, 0), (2, 0), (3, 2), (5, 2)):
         for n in range(4):
             assert abs(y[r, n] - sum(x[r, k] * w[e, n, k] for k in range(5))) < 1e-12
+
+
+def test_pointers_off_their_elements_are_refused(bq):
+    """A base that is no multiple of its element's size never reaches a kernel."""
+    for name in ("branch", "residual", "residual_out", "h", "pre_weight", "post_weight", "gate"):
+        assert _norm(bq, **{name: P + 1}) == INVALID
+    assert _norm(bq, residual_dtype=bq.FP32, residual=P + 2, residual_out=P) == INVALID
+    assert _quant(bq, x=P + 1) == INVALID
+    lib = bq._lib()
+    for x, w, y, yd in ((P + 1, P, P, bq.BF16), (P, P + 1, P, bq.BF16), (P, P, P + 1, bq.BF16), (P, P, P + 2, bq.FP32)):
+        assert lib.moe_grouped_matmul(x, 64, w, 64, 0, None, 4, 1, 64, 32, bq.BF16, y, 32, yd, None) == INVALID
+    assert lib.moe_int8_matmul(P, 64, P, P, 64, 0, P, None, 4, 1, 64, 32, P + 2, 32, bq.FP32, None) == INVALID
