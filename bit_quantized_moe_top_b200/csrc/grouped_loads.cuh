@@ -63,6 +63,24 @@ struct Chunk16 {
   }
 };
 
+// A CTA's work in the order in which it is done: its tiles, whole or, where sums
+// are taken in chunks, a chunk of K at a time (added up in y).
+template <bool CHUNKS>
+struct PartOf {
+  int tile, first, end, total, nk;
+  __device__ __forceinline__ PartOf(int total_, int nk_)
+      : tile((int)blockIdx.x - (int)gridDim.x), first(nk_), end(nk_), total(total_), nk(nk_) {}
+  __device__ __forceinline__ bool next(bool ok) {
+    first = end;
+    if (first >= nk) {
+      first = 0;
+      tile += gridDim.x;
+    }
+    end = CHUNKS ? min(first + kChunk, nk) : nk;
+    return ok && tile < total;
+  }
+};
+
 template <bool I8, typename TO>
 __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const __grid_constant__ TcArgs a) {
   extern __shared__ uint8_t raw[];
@@ -73,6 +91,7 @@ __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const _
   __shared__ int abort_s;
   constexpr int ES = I8 ? 1 : 2;
   constexpr uint32_t kCols = 128;
+  using Part = PartOf<kSumChunks<I8, TO>>;
   constexpr int kStage = kABytes + 128 * kRowBytes;
   const uint32_t pad = (1024u - (smem_u32(raw) & 1023u)) & 1023u;
   uint8_t* sm = raw + pad;
@@ -114,11 +133,12 @@ __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const _
     uint32_t* stage = reinterpret_cast<uint32_t*>(sm) + warp * 512;
     int slot = 0, round = 0, it = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < total && ok; i += gridDim.x, ++it) {
-      const Tile t = tile_of<1>(g, a, i);
+    for (Part q(total, nk); q.next(ok); ++it) {
+      const int first = q.first, end = q.end;
+      const Tile t = tile_of<1>(g, a, q.tile);
       const uint8_t* x = static_cast<const uint8_t*>(a.g.x) + (long long)t.r0 * a.g.ldx * ES;
       const uint8_t* w = static_cast<const uint8_t*>(a.g.w) + ((long long)t.e * a.g.ldwe + (long long)t.f0 * a.g.ldw) * ES;
-      for (int kb = 0; kb < nk; ++kb) {
+      for (int kb = first; kb < end; ++kb) {
         const long long b = (long long)kb * kRowBytes + lc * 16;
         Chunk16<ES> cw[4], cx[4];
 #pragma unroll
@@ -157,7 +177,7 @@ __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const _
         uint32_t v[32];
         tmem_ld32_nw(tmem + ((uint32_t)(quarter * 32) << 16) + c0, v);
         tmem_wait_ld(v);
-        store_chunk<TO, I8>(a, t, c0, v, ws, stage, xs_s[warp], ch0, lane);
+        store_chunk<TO, I8>(a, t, c0, v, ws, stage, xs_s[warp], ch0, lane, kSumChunks<I8, TO> && first > 0);
       }
       tc_fence_before();
       __syncwarp();
@@ -169,14 +189,15 @@ __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const _
   } else {
     int slot = 0, ph = 0, it = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < total && ok; i += gridDim.x, ++it) {
-      const Tile t = tile_of<1>(g, a, i);
+    for (Part q(total, nk); q.next(ok); ++it) {
+      const int first = q.first, end = q.end;
+      const Tile t = tile_of<1>(g, a, q.tile);
       ok = it == 0 || role_wait(acc_empty, (it - 1) & 1, status, a.g.wait_ns, aborted);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       const uint32_t idesc = a.idesc | ((uint32_t)(t.n >> 3) << 17);
-      for (int kb = 0; kb < nk; ++kb) {
+      for (int kb = first; kb < end; ++kb) {
         ok = role_wait(full(slot), ph, status, a.g.wait_ns, aborted);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -184,9 +205,9 @@ __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const _
         if (elect_one()) {
           const uint64_t ad = sw128_desc(sbase + slot * kStage), bd = sw128_desc(sbase + slot * kStage + kABytes);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_ss<1, I8>(tmem, ad + 2 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
+          for (int k = 0; k < 4; ++k) mma_ss<1, I8>(tmem, ad + 2 * k, bd + 2 * k, idesc, kb > first || k > 0);
           commit<1>(empty(slot));
-          if (kb == nk - 1) commit<1>(acc_full);
+          if (kb == end - 1) commit<1>(acc_full);
         }
         __syncwarp();
         if (++slot == kStagesLoads) {

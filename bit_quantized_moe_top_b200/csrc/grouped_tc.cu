@@ -47,6 +47,16 @@ constexpr int kMaxStagesTc = 10;
 constexpr int kBandTc = 8;                     // row tiles that share a sweep over the channels
 constexpr int kStagingBytes = kEpiWarps * 2048;
 
+// The tensor cores add to their fp32 accumulators with truncation, whose error
+// grows with the number of additions: relative to the output 2.5e-6 over K =
+// 2048, four times that over 8192, where sums rounded to nearest stay at 1e-6.
+// A 16-bit output's own rounding hides that; for fp32 outputs the accumulators
+// are emptied every kChunk stages (512 values of K) and added up in fp32
+// registers, rounded to nearest: 6.5e-7 at any K.
+constexpr int kChunk = 8;
+template <bool I8, typename TO>
+constexpr bool kSumChunks = !I8 && sizeof(TO) == 4;
+
 struct TcArgs {
   CUtensorMap map_w;   // [E][N][K], box 128 rows
   CUtensorMap map_x[4];  // [rows][K], boxes of 32, 64, 96 and 128 rows as far as nmax needs them: one copy per stage
@@ -229,10 +239,10 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
 // One warp's 32 channels (lane = channel) of 32 rows to y. 16-bit outputs
 // cross the warp's 2 KiB of shared memory as pairs of rows, so that a store
 // covers four rows of 32 channels, 8 bytes a lane; 32-bit outputs go out
-// directly, one row of 32 channels per store.
+// directly, one row of 32 channels per store, or are added to what is there.
 template <typename TO, bool I8>
 __device__ __forceinline__ void store_chunk(const TcArgs& a, const Tile& t, int c0, const uint32_t (&v)[32], float ws,
-                                            uint32_t* stage, float* xs, int ch0, int lane) {
+                                            uint32_t* stage, float* xs, int ch0, int lane, bool add = false) {
   float sc[32];
   if constexpr (I8) {
     xs[lane] = c0 + lane < t.live ? a.g.xs[t.r0 + c0 + lane] : 0.f;
@@ -250,7 +260,11 @@ __device__ __forceinline__ void store_chunk(const TcArgs& a, const Tile& t, int 
   if constexpr (sizeof(TO) == 4) {
     if (ch0 + lane < a.g.N) {
       float* y = static_cast<float*>(a.g.y) + (long long)(t.r0 + c0) * a.g.ldy + ch0 + lane;
-      if (rows >= 32) {
+      if (add) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j < rows) y[j * a.g.ldy] += scaled<I8>(v[j], I8 ? sc[j] : 0.f);
+      } else if (rows >= 32) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) y[j * a.g.ldy] = scaled<I8>(v[j], I8 ? sc[j] : 0.f);
       } else {
@@ -310,6 +324,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
   constexpr int kUnitCols = CG == 2 ? 256 : 128;  // TMEM columns of one accumulator
   constexpr uint32_t kCols = 2 * kUnitCols;
   constexpr int kElem = I8 ? 128 : 64;            // elements per 128-byte row
+  constexpr bool kSum = kSumChunks<I8, TO>;
   const uint32_t pad = (1024u - (smem_u32(raw) & 1023u)) & 1023u;
   uint8_t* sm = raw + pad;
   const uint32_t sbase = smem_u32(sm);
@@ -403,33 +418,35 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
     if (!ok) *aborted = 1;
   } else if (warp == 1) {
     if (CG == 1 || rank == 0) {
-      int slot = 0, ph = 0, it = 0;
+      int slot = 0, ph = 0, u = 0;  // u: accumulators filled so far
       bool ok = true;
-      for (int i = cluster; i < total && ok; i += nclusters, ++it) {
+      for (int i = cluster; i < total && ok; i += nclusters) {
         const Tile t = tile_of<CG>(g, a, i);
-        const int buf = it & 1;
-        ok = it < 2 || role_wait(acc_empty(buf), ((it >> 1) - 1) & 1, status, a.g.wait_ns, aborted);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
         const uint32_t idesc = a.idesc | ((uint32_t)(t.n >> 3) << 17);
-        const uint32_t d = tmem + buf * kUnitCols;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          ok = role_wait(full(slot), ph, status, a.g.wait_ns, aborted);
+        for (int kb = kb0; kb < kb1 && ok; ++u) {
+          const int first = kb, end = kSum ? min(kb + kChunk, kb1) : kb1, buf = u & 1;
+          ok = u < 2 || role_wait(acc_empty(buf), ((u >> 1) - 1) & 1, status, a.g.wait_ns, aborted);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          if (elect_one()) {
-            const uint64_t ad = sw128_desc(sbase + slot * stage_bytes), bd = sw128_desc(sbase + slot * stage_bytes + kABytes);
+          const uint32_t d = tmem + buf * kUnitCols;
+          for (; kb < end; ++kb) {
+            ok = role_wait(full(slot), ph, status, a.g.wait_ns, aborted);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t ad = sw128_desc(sbase + slot * stage_bytes), bd = sw128_desc(sbase + slot * stage_bytes + kABytes);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_ss<CG, I8>(d, ad + 2 * k, bd + 2 * k, idesc, kb > kb0 || k > 0);
-            commit<CG>(empty(slot));
-            if (kb == kb1 - 1) commit<CG>(acc_full(buf));
-          }
-          __syncwarp();
-          if (++slot == a.stages) {
-            slot = 0;
-            ph ^= 1;
+              for (int k = 0; k < 4; ++k) mma_ss<CG, I8>(d, ad + 2 * k, bd + 2 * k, idesc, kb > first || k > 0);
+              commit<CG>(empty(slot));
+              if (kb == end - 1) commit<CG>(acc_full(buf));
+            }
+            __syncwarp();
+            if (++slot == a.stages) {
+              slot = 0;
+              ph ^= 1;
+            }
           }
         }
       }
@@ -448,57 +465,115 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     uint32_t* stage = reinterpret_cast<uint32_t*>(tail) + (warp - 2) * 512;
     float* xs = xs_s[warp - 2];
-    int it = 0;
-    for (int i = cluster; i < total; i += nclusters, ++it) {
+    int u = 0;
+    auto filled = [&](int buf) {
+      const bool ok = role_wait(acc_full(buf), (u >> 1) & 1, status, a.g.wait_ns, aborted);
+      return __all_sync(0xffffffffu, ok);
+    };
+    auto release = [&](int buf) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 2) arrive_cluster(map_rank(acc_empty(buf), lead));
+        else mbar_arrive(acc_empty(buf));
+      }
+    };
+    for (int i = cluster; i < total; i += nclusters) {
       const Tile t = tile_of<CG>(g, a, i);
-      const int buf = it & 1;
       const int ch0 = t.f0 + (CG == 2 ? (int)rank * 128 : 0) + quarter * 32, ch = ch0 + lane;
+      const bool split = CG == 1 && a.S > 1;
+      // Of a split tile the partial sums of columns [q c, q c + c) go to CTA q,
+      // slot [rank]; in a slot four columns of a channel lie together, 16 bytes
+      // a lane.
+      const int c = split ? t.n / a.S : t.n;
+      const uint32_t part = smem_u32(tail) + (uint32_t)((int)rank * c * 512 + (quarter * 32 + lane) * 16);
+      auto send = [&](int col, const uint32_t* v) {
+        const int q = col / c;
+        st_cluster_v4(map_rank(part + (uint32_t)(col - q * c) * 512, q), v);
+      };
       float ws = 0.f;
       if constexpr (I8)
         if (ch < a.g.N) ws = a.g.ws[(long long)t.e * a.g.N + ch];
-      bool ok = role_wait(acc_full(buf), (it >> 1) & 1, status, a.g.wait_ns, aborted);
-      if (!__all_sync(0xffffffffu, ok)) {
+      bool ok = true;
+      if constexpr (kSum) {
+        constexpr int kParts = kUnitCols / 64;
+        uint32_t sum[kParts][32];
+        for (int kb = kb0; kb < kb1; kb += kChunk, ++u) {
+          const int buf = u & 1;
+          ok = filled(buf);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + buf * kUnitCols + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) {
+            const int c0 = half * 32 + p * 64;
+            if (c0 >= t.n) break;
+            if (kb == kb0) {
+              tmem_ld32_nw(d + c0, sum[p]);
+              tmem_wait_ld(sum[p]);
+            } else {
+              uint32_t v[32];
+              tmem_ld32_nw(d + c0, v);
+              tmem_wait_ld(v);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sum[p][j] = __float_as_uint(__uint_as_float(sum[p][j]) + __uint_as_float(v[j]));
+            }
+          }
+          release(buf);
+        }
+        if (ok) {
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) {
+            const int c0 = half * 32 + p * 64;
+            if (c0 >= t.n) break;
+            if (split) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4)
+                if (c0 + j < t.n) send(c0 + j, sum[p] + j);
+            } else {
+              store_chunk<TO, I8>(a, t, c0, sum[p], ws, stage, xs, ch0, lane);
+            }
+          }
+        }
+      } else {
+        const int buf = u & 1;
+        ok = filled(buf);
+        if (ok) {
+          tc_fence_after();
+          const uint32_t d = tmem + buf * kUnitCols + ((uint32_t)(quarter * 32) << 16);
+          if (!split) {
+            // the next chunk's load is in flight while a chunk is stored
+            uint32_t v[2][32];
+            const int c_first = half * 32;
+            if (c_first < t.n) tmem_ld32_nw(d + c_first, v[0]);
+#pragma unroll 1
+            for (int c0 = c_first; c0 < t.n; c0 += 128) {
+              tmem_wait_ld(v[0]);
+              if (c0 + 64 < t.n) tmem_ld32_nw(d + c0 + 64, v[1]);
+              store_chunk<TO, I8>(a, t, c0, v[0], ws, stage, xs, ch0, lane);
+              if (c0 + 64 < t.n) {
+                tmem_wait_ld(v[1]);
+                if (c0 + 128 < t.n) tmem_ld32_nw(d + c0 + 128, v[0]);
+                store_chunk<TO, I8>(a, t, c0 + 64, v[1], ws, stage, xs, ch0, lane);
+              }
+            }
+          } else {
+            for (int c0 = half * 16; c0 < t.n; c0 += 32) {
+              uint32_t v[16];
+              tmem_ld16(d + c0, v);
+#pragma unroll
+              for (int j = 0; j < 16; j += 4) send(c0 + j, v + j);
+            }
+          }
+          release(buf);
+        }
+        ++u;
+      }
+      if (!ok) {
         *aborted = 1;
         break;
       }
-      tc_fence_after();
-      const uint32_t d = tmem + buf * kUnitCols + ((uint32_t)(quarter * 32) << 16);
-      if (CG == 2 || a.S == 1) {
-        // the next chunk's load is in flight while a chunk is stored
-        uint32_t v[2][32];
-        const int c_first = half * 32;
-        if (c_first < t.n) tmem_ld32_nw(d + c_first, v[0]);
-#pragma unroll 1
-        for (int c0 = c_first; c0 < t.n; c0 += 128) {
-          tmem_wait_ld(v[0]);
-          if (c0 + 64 < t.n) tmem_ld32_nw(d + c0 + 64, v[1]);
-          store_chunk<TO, I8>(a, t, c0, v[0], ws, stage, xs, ch0, lane);
-          if (c0 + 64 < t.n) {
-            tmem_wait_ld(v[1]);
-            if (c0 + 128 < t.n) tmem_ld32_nw(d + c0 + 128, v[0]);
-            store_chunk<TO, I8>(a, t, c0 + 64, v[1], ws, stage, xs, ch0, lane);
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (CG == 2) arrive_cluster(map_rank(acc_empty(buf), lead));
-          else mbar_arrive(acc_empty(buf));
-        }
-      } else {
-        // Partial sums of columns [q c, q c + c) go to CTA q, slot [rank]; in
-        // a slot four columns of a channel lie together, 16 bytes a lane.
-        const int c = t.n / a.S;
-        const uint32_t part = smem_u32(tail) + (uint32_t)((int)rank * c * 512 + (quarter * 32 + lane) * 16);
-        for (int c0 = half * 16; c0 < t.n; c0 += 32) {
-          uint32_t v[16];
-          tmem_ld16(d + c0, v);
-#pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const int q = (c0 + j) / c;
-            st_cluster_v4(map_rank(part + (uint32_t)(c0 + j - q * c) * 512, q), v + j);
-          }
-        }
+      if (split) {
         __syncwarp();
         if (lane < a.S) arrive_cluster(map_rank(summed, lane));
         ok = mbar_wait(summed, 0, status, a.g.wait_ns);

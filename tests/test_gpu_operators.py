@@ -421,6 +421,21 @@ def test_grouped_matmul_gaussian(bq, dtype, counts, N, K):
     check(rounded, ref, tol + half_step(DT[dtype], np.abs(ref) + tol), dtype)
 
 
+@pytest.mark.parametrize("R,N,K", [(8, 512, 8192), (600, 4096, 8192), (300, 1024, 8192), (200, 256, 8191), (3, 200, 7168)])
+def test_grouped_matmul_long_sums(bq, R, N, K):
+    """The error of fp32 outputs does not grow with K. Accumulators truncate, 32
+    times in 512 values of K, by at most 2^-23 of a partial sum each time, whose
+    size is on average two thirds of the last: 32 * 2^-23 * 2 / 3 of a chunk's
+    sum. Chunks are independent, so the whole output has the same relative error,
+    and sqrt(chunks) roundings of 2^-24 more. Without chunks it would be 16 times
+    as much at K = 8192."""
+    gen = seeded(R, N, K)
+    x, w = rnd(gen, (R, K), 1.0, torch.float16), rnd(gen, (1, N, K), 0.02, torch.float16)
+    got = bq.moe_grouped_matmul(x, w, out_dtype=torch.float32).double()
+    ref = x.double() @ w[0].double().t()
+    assert float((got - ref).norm() / ref.norm()) <= 32 * 2.0 ** -23 * 2 / 3 + U * (K / 512) ** 0.5
+
+
 @pytest.mark.parametrize("out", ["bf16", "fp32"])
 def test_int8_matmul_scales(bq, out):
     gen = seeded(11)
