@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -104,7 +105,7 @@ def _lib() -> ctypes.CDLL:
         lib.moe_plan_reduce.argtypes = [PB, I, ctypes.c_longlong, ctypes.c_float, IP, LP]
         lib.moe_plan_restore.argtypes = [PB, I, IP, ctypes.c_longlong, ctypes.c_float, IP, LP]
         LL = ctypes.c_longlong
-        lib.moe_block_norm.argtypes = [ctypes.POINTER(BlockNormArgs), P]
+        lib.moe_block_norm.argtypes = [P, P]  # a BlockNormArgs by reference, or its bytes
         lib.moe_quantize_rows.argtypes = [P, LL, I, I, P, I, I, P, LL, P, P]
         lib.moe_int8_matmul.argtypes = [P, LL, P, P, LL, LL, P, P, I, I, I, I, P, LL, I, P]
         lib.moe_grouped_matmul.argtypes = [P, LL, P, LL, LL, P, I, I, I, I, I, P, LL, I, P]
@@ -320,6 +321,7 @@ def moe_layer_destroy(layer: int) -> None:
 # most of the time): the usual case, a contiguous tensor of the expected shape,
 # is looked at first, outputs made here are not checked, and no views are made.
 
+_NORM_ARGS = struct.Struct("@iiiiPqiiPPPPqiiPqffPffPqPq")  # the fields of BlockNormArgs
 _ENV = None
 
 
@@ -404,54 +406,56 @@ def moe_block_norm(residual=None, branch=None, *, w_pre=None, w_post=None, gate=
         T = inv_pos.shape[0]
     dt = branch.dtype if branch is not None else w_pre.dtype if w_pre is not None else residual.dtype
     rdt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else dt
-    a = BlockNormArgs(T, K, codes.get(dt, -1), codes.get(rdt, -1))
-    a.residual_scale, a.branch_scale, a.eps, a.weight_offset = residual_scale, branch_scale, eps, weight_offset
+    res = y = inv = pw = post = pre = g = r_out = h = 0     # addresses
+    ld_res = ld_y = rows = k = ld_g = g_chan = ld_out = ld_h = 0
+    like = None  # a new output is made like the contiguous residual, which costs least
     if residual is not None:
-        a.residual_stride = _rows(residual, f, index, T, K)
-        a.residual = residual.data_ptr()
-    # a new output is like the contiguous residual, whose copy costs least
-    like = residual if residual is not None and stream is None and residual.is_contiguous() else None
-    if residual_out is not None:
-        _require(residual_out.dtype is rdt, f)
-        a.residual_out_stride = _rows(residual_out, f, index, T, K)
-        a.residual_out = residual_out.data_ptr()
-    elif branch is not None:
-        residual_out = torch.empty_like(like) if like is not None else _new((T, K), rdt, lead.device, stream)
-        a.residual_out_stride, a.residual_out = K, residual_out.data_ptr()
-    if h_out is not None:
-        _require(h_out.dtype is dt, f)
-        a.h_stride = _rows(h_out, f, index, T, K)
-        a.h = h_out.data_ptr()
-    elif w_pre is not None:
-        h_out = (torch.empty_like(like, dtype=dt) if like is not None else
-                 _new((T, K), dt, lead.device, stream))
-        a.h_stride, a.h = K, h_out.data_ptr()
+        res = residual.data_ptr()
+        if residual.is_contiguous():
+            ld_res = K
+            like = residual if stream is None else None
+        else:
+            ld_res = _rows(residual, f, index, T, K)
     if branch is not None:
-        a.branch_stride = _rows(branch, f, index, T if inv_pos is None else None, K)
-        a.branch, a.branch_rows = branch.data_ptr(), branch.shape[0]
+        ld_y = _rows(branch, f, index, T if inv_pos is None else None, K)
+        y, rows = branch.data_ptr(), branch.shape[0]
     if inv_pos is not None or pair_weights is not None:
         _require(inv_pos is not None and pair_weights is not None and inv_pos.dim() == 2 and inv_pos.shape[1] >= 1, f)
-        a.pairs = k = inv_pos.shape[1]
-        a.inv_pos = _flat(inv_pos, f, index, torch.int32, (T, k))
-        a.pair_weights = _flat(pair_weights, f, index, torch.float32, (T, k))
+        k = inv_pos.shape[1]
+        inv = _flat(inv_pos, f, index, torch.int32, (T, k))
+        pw = _flat(pair_weights, f, index, torch.float32, (T, k))
     if w_post is not None:
-        a.post_weight = _flat(w_post, f, index, dt, (K,))
+        post = _flat(w_post, f, index, dt, (K,))
     if w_pre is not None:
-        a.pre_weight = _flat(w_pre, f, index, dt, (K,))
+        pre = _flat(w_pre, f, index, dt, (K,))
     if gate is not None:
         if gate.dim() == 1:
-            a.gate = _flat(gate, f, index, dt, (K,))
-            a.gate_channel_stride = 1
+            g, g_chan = _flat(gate, f, index, dt, (K,)), 1
         else:
             _require(gate.dim() == 2 and gate.dtype is dt, f)
             width = gate.shape[1]
             _require(width == 1 or width == K, f)
-            a.gate_token_stride = _rows(gate, f, index, T, width)
-            a.gate_channel_stride = 0 if width == 1 else 1
-            a.gate = gate.data_ptr()
-        a.gate_sigmoid = 1 if gate_sigmoid else 0
+            g, ld_g, g_chan = gate.data_ptr(), _rows(gate, f, index, T, width), 0 if width == 1 else 1
+    if residual_out is not None:
+        _require(residual_out.dtype is rdt, f)
+        ld_out, r_out = _rows(residual_out, f, index, T, K), residual_out.data_ptr()
+    elif branch is not None:
+        residual_out = torch.empty_like(like) if like is not None else _new((T, K), rdt, lead.device, stream)
+        ld_out, r_out = K, residual_out.data_ptr()
+    if h_out is not None:
+        _require(h_out.dtype is dt, f)
+        ld_h, h = _rows(h_out, f, index, T, K), h_out.data_ptr()
+    elif w_pre is not None:
+        h_out = torch.empty_like(like, dtype=dt) if like is not None else _new((T, K), dt, lead.device, stream)
+        ld_h, h = K, h_out.data_ptr()
     if T > 0:
-        _call(index, stream, f, lib.moe_block_norm, ctypes.byref(a))
+        try:
+            args = _NORM_ARGS.pack(T, K, codes.get(dt, -1), codes.get(rdt, -1), y, ld_y, rows, k, inv, pw, post, g, ld_g,
+                                   g_chan, 1 if gate_sigmoid else 0, res, ld_res, residual_scale, branch_scale, pre, eps,
+                                   weight_offset, r_out, ld_out, h, ld_h)
+        except (struct.error, OverflowError):
+            raise MoEError(1, f) from None
+        _call(index, stream, f, lib.moe_block_norm, args)
     return residual_out, h_out
 
 
@@ -463,7 +467,7 @@ def moe_quantize_rows(x, src_rows=None, codes=None, scales=None, stream: Optiona
     _require(x.dim() == 2 and x.is_cuda, f)
     index = x.get_device()
     M, K = x.shape
-    ldx = _rows(x, f, index, M, K)
+    ldx = K if x.is_contiguous() else _rows(x, f, index, M, K)
     R, src = M, None
     if src_rows is not None:
         _require(src_rows.dim() == 1, f)
@@ -491,7 +495,7 @@ def _product(f, x, w, offsets, out_dtype, out, stream):
         raise MoEError(1, f)
     index = x.get_device()
     R, K = x.shape
-    ldx = _rows(x, f, index, R, K)
+    ldx = K if x.is_contiguous() else _rows(x, f, index, R, K)
     shape, strides = w.shape, w.stride()
     if len(shape) == 2:
         E, N = 1, shape[0]

@@ -162,3 +162,15 @@ def test_pointers_off_their_elements_are_refused(bq):
     for x, w, y, yd in ((P + 1, P, P, bq.BF16), (P, P + 1, P, bq.BF16), (P, P, P + 1, bq.BF16), (P, P, P + 2, bq.FP32)):
         assert lib.moe_grouped_matmul(x, 64, w, 64, 0, None, 4, 1, 64, 32, bq.BF16, y, 32, yd, None) == INVALID
     assert lib.moe_int8_matmul(P, 64, P, P, 64, 0, P, None, 4, 1, 64, 32, P + 2, 32, bq.FP32, None) == INVALID
+
+
+def test_packed_norm_arguments_match_the_struct(bq):
+    """The binding packs moe_block_norm_t as bytes: same size and field offsets as the ctypes struct."""
+    import struct
+    assert bq._NORM_ARGS.size == ctypes.sizeof(bq.BlockNormArgs)
+    codes = {ctypes.c_int: "i", ctypes.c_void_p: "P", ctypes.c_longlong: "q", ctypes.c_float: "f"}
+    fmt = "@"
+    for name, typ in bq.BlockNormArgs._fields_:
+        fmt += codes[typ]
+        assert struct.calcsize(fmt) - struct.calcsize("@" + codes[typ]) == getattr(bq.BlockNormArgs, name).offset, name
+    assert fmt == bq._NORM_ARGS.format
