@@ -579,6 +579,36 @@ def test_block_norm_refused_forms(bq):
         assert ei.value.status == 1
 
 
+@pytest.mark.parametrize("op", ["bf16", "int8"])
+@pytest.mark.parametrize("R,N,K,pad", [
+    (700, 2048, 2048, 0),    # CTA pairs
+    (8, 256, 4096, 0),       # K split over a cluster
+    (100, 128, 2048, 3),     # ordinary loads
+])
+def test_products_wait_limit_then_recovery(bq, op, R, N, K, pad):
+    """With a limit of 1 ns the first wait between roles that is not over yet gives
+    up: the call returns, the status says so once, and the next call is right."""
+    gen = seeded(R, N, K)
+    x, w, xs, ws = operands(op, gen, R, 1, N, K, pad)
+    want = product(bq, op, x, w, None, torch.float32, xs, ws)
+    assert bq.moe_op_sync_status() == 0
+    bq.moe_op_set_wait_limit(1)
+    try:
+        seen = []
+        for _ in range(5):
+            product(bq, op, x, w, None, torch.float32, xs, ws)
+            seen.append(bq.moe_op_sync_status())
+            if seen[-1] == 8:
+                break
+    finally:
+        bq.moe_op_set_wait_limit(0)
+    assert seen[-1] == 8 and set(seen) <= {0, 8}, seen
+    assert bq.moe_op_sync_status() == 0
+    for _ in range(3):
+        assert torch.equal(product(bq, op, x, w, None, torch.float32, xs, ws), want)
+    assert bq.moe_op_sync_status() == 0
+
+
 # ---------------------------------------------------------------------------
 # streams, graphs and the calls together
 # ---------------------------------------------------------------------------

@@ -174,3 +174,11 @@ def test_packed_norm_arguments_match_the_struct(bq):
         fmt += codes[typ]
         assert struct.calcsize(fmt) - struct.calcsize("@" + codes[typ]) == getattr(bq.BlockNormArgs, name).offset, name
     assert fmt == bq._NORM_ARGS.format
+
+
+def test_product_extents(bq):
+    lib = bq._lib()
+    big = (1 << 29) + 1
+    for rows, K, N in ((big, 64, 32), (4, big, 32), (4, 64, big)):
+        assert lib.moe_grouped_matmul(P, K, P, K, 0, None, rows, 1, K, N, bq.BF16, P, N, bq.BF16, None) == TOO_LARGE
+        assert lib.moe_int8_matmul(P, K, P, P, K, 0, P, None, rows, 1, K, N, P, N, bq.BF16, None) == TOO_LARGE
