@@ -10,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from typing import Optional, Sequence
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -105,7 +104,7 @@ def _lib() -> ctypes.CDLL:
         lib.moe_plan_reduce.argtypes = [PB, I, ctypes.c_longlong, ctypes.c_float, IP, LP]
         lib.moe_plan_restore.argtypes = [PB, I, IP, ctypes.c_longlong, ctypes.c_float, IP, LP]
         LL = ctypes.c_longlong
-        lib.moe_block_norm.argtypes = [P, P]  # a BlockNormArgs by reference, or its bytes
+        lib.moe_block_norm.argtypes = [ctypes.POINTER(BlockNormArgs), P]
         lib.moe_quantize_rows.argtypes = [P, LL, I, I, P, I, I, P, LL, P, P]
         lib.moe_int8_matmul.argtypes = [P, LL, P, P, LL, LL, P, P, I, I, I, I, P, LL, I, P]
         lib.moe_grouped_matmul.argtypes = [P, LL, P, LL, LL, P, I, I, I, I, I, P, LL, I, P]
@@ -317,71 +316,24 @@ def moe_layer_destroy(layer: int) -> None:
 # stand-alone operators around the experts
 # ---------------------------------------------------------------------------
 
-# The checks below are written for short calls (of a one-token call they are
-# most of the time): the usual case, a contiguous tensor of the expected shape,
-# is looked at first, outputs made here are not checked, and no views are made.
-
-_NORM_ARGS = struct.Struct("@iiiiPqiiPPPPqiiPqffPffPqPq")  # the fields of BlockNormArgs
-_ENV = None
+_BINDING = None
 
 
-def _env() -> tuple:
-    """(torch, the library, its codes of the torch dtypes), looked up once."""
-    global _ENV
-    if _ENV is None:
-        import torch
-        _ENV = torch, _lib(), {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
-    return _ENV
-
-
-def _require(ok, where: str):
-    if not ok:
-        raise MoEError(1, where)
-
-
-def _call(index: int, stream, where: str, fn, *args) -> None:
-    """fn(*args, stream) with device ``index`` current, on its current stream unless one is given."""
-    torch = _ENV[0]
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
-    if index == torch._C._cuda_getDevice():
-        status = fn(*args, stream)
-    else:
-        with torch.cuda.device(index):
-            status = fn(*args, stream)
-    if status != MOE_OK:
-        raise MoEError(status, where)
-
-
-def _new(shape, dtype, device, stream):
-    """An output, from the memory pool of the stream that will write it."""
-    torch = _ENV[0]
-    if stream is None:
-        return torch.empty(*shape, dtype=dtype, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device)):
-        return torch.empty(*shape, dtype=dtype, device=device)
-
-
-def _rows(t, where: str, index: int, n, width: int) -> int:
-    """Row stride of a 2-D tensor [n (None: any), width] on device ``index`` whose rows are contiguous."""
-    if t.get_device() != index:
-        raise MoEError(1, where)
-    if t.is_contiguous() and t.shape == (n, width):
-        return width
-    if t.dim() != 2:
-        raise MoEError(1, where)
-    rows, cols = t.shape
-    ld, unit = t.stride()
-    if cols != width or (unit != 1 and cols != 1) or (n is not None and rows != n):
-        raise MoEError(1, where)
-    return ld
-
-
-def _flat(t, where: str, index: int, dtype, shape) -> int:
-    """Address of a contiguous tensor of the given type, shape and device."""
-    if t.get_device() != index or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise MoEError(1, where)
-    return t.data_ptr()
+def _ops():
+    """The compiled calls on torch tensors (csrc/binding.cpp): they check the
+    tensors, make the outputs, and call the library on the tensors' device."""
+    global _BINDING
+    if _BINDING is None:
+        import torch  # noqa: F401  (the binding links against its libraries)
+        _lib()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ImportError(f"the operators' binding cannot be loaded ({e}): build it with "
+                              "bit_quantized_moe_top_b200.build.build()") from e
+        _binding.set_error(MoEError)
+        _BINDING = _binding
+    return _BINDING
 
 
 def moe_block_norm(residual=None, branch=None, *, w_pre=None, w_post=None, gate=None, gate_sigmoid: bool = False,
@@ -395,125 +347,16 @@ def moe_block_norm(residual=None, branch=None, *, w_pre=None, w_post=None, gate=
     int32 [T, k] and pair_weights fp32 [T, k]; w_post, w_pre [K]; gate [K] (per
     channel), [T, 1] (per token) or [T, K]. Without w_pre no h is made; without
     a branch no residual_out is made unless one is given. residual_out may be
-    ``residual`` itself."""
-    torch, lib, codes = _ENV or _env()
-    f = "moe_block_norm"
-    lead = residual if residual is not None else branch
-    _require(lead is not None and lead.dim() == 2 and lead.is_cuda, f)
-    index = lead.get_device()
-    T, K = lead.shape
-    if residual is None and inv_pos is not None:
-        T = inv_pos.shape[0]
-    dt = branch.dtype if branch is not None else w_pre.dtype if w_pre is not None else residual.dtype
-    rdt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else dt
-    res = y = inv = pw = post = pre = g = r_out = h = 0     # addresses
-    ld_res = ld_y = rows = k = ld_g = g_chan = ld_out = ld_h = 0
-    like = None  # a new output is made like the contiguous residual, which costs least
-    if residual is not None:
-        res = residual.data_ptr()
-        if residual.is_contiguous():
-            ld_res = K
-            like = residual if stream is None else None
-        else:
-            ld_res = _rows(residual, f, index, T, K)
-    if branch is not None:
-        ld_y = _rows(branch, f, index, T if inv_pos is None else None, K)
-        y, rows = branch.data_ptr(), branch.shape[0]
-    if inv_pos is not None or pair_weights is not None:
-        _require(inv_pos is not None and pair_weights is not None and inv_pos.dim() == 2 and inv_pos.shape[1] >= 1, f)
-        k = inv_pos.shape[1]
-        inv = _flat(inv_pos, f, index, torch.int32, (T, k))
-        pw = _flat(pair_weights, f, index, torch.float32, (T, k))
-    if w_post is not None:
-        post = _flat(w_post, f, index, dt, (K,))
-    if w_pre is not None:
-        pre = _flat(w_pre, f, index, dt, (K,))
-    if gate is not None:
-        if gate.dim() == 1:
-            g, g_chan = _flat(gate, f, index, dt, (K,)), 1
-        else:
-            _require(gate.dim() == 2 and gate.dtype is dt, f)
-            width = gate.shape[1]
-            _require(width == 1 or width == K, f)
-            g, ld_g, g_chan = gate.data_ptr(), _rows(gate, f, index, T, width), 0 if width == 1 else 1
-    if residual_out is not None:
-        _require(residual_out.dtype is rdt, f)
-        ld_out, r_out = _rows(residual_out, f, index, T, K), residual_out.data_ptr()
-    elif branch is not None:
-        residual_out = torch.empty_like(like) if like is not None else _new((T, K), rdt, lead.device, stream)
-        ld_out, r_out = K, residual_out.data_ptr()
-    if h_out is not None:
-        _require(h_out.dtype is dt, f)
-        ld_h, h = _rows(h_out, f, index, T, K), h_out.data_ptr()
-    elif w_pre is not None:
-        h_out = torch.empty_like(like, dtype=dt) if like is not None else _new((T, K), dt, lead.device, stream)
-        ld_h, h = K, h_out.data_ptr()
-    if T > 0:
-        try:
-            args = _NORM_ARGS.pack(T, K, codes.get(dt, -1), codes.get(rdt, -1), y, ld_y, rows, k, inv, pw, post, g, ld_g,
-                                   g_chan, 1 if gate_sigmoid else 0, res, ld_res, residual_scale, branch_scale, pre, eps,
-                                   weight_offset, r_out, ld_out, h, ld_h)
-        except (struct.error, OverflowError):
-            raise MoEError(1, f) from None
-        _call(index, stream, f, lib.moe_block_norm, args)
-    return residual_out, h_out
+    ``residual`` itself. Forward only, like the layer."""
+    return (_BINDING or _ops()).block_norm(residual, branch, w_pre, w_post, gate, gate_sigmoid, residual_scale,
+                                           branch_scale, eps, weight_offset, inv_pos, pair_weights, residual_out, h_out,
+                                           stream)
 
 
 def moe_quantize_rows(x, src_rows=None, codes=None, scales=None, stream: Optional[int] = None):
     """Rows of x (bf16 or fp16 [M, K]), or the rows src_rows (int32 [R]) selects,
     as 8-bit codes with one scale each; returns (codes int8 [R, K], scales fp32 [R])."""
-    torch, lib, dtypes = _ENV or _env()
-    f = "moe_quantize_rows"
-    _require(x.dim() == 2 and x.is_cuda, f)
-    index = x.get_device()
-    M, K = x.shape
-    ldx = K if x.is_contiguous() else _rows(x, f, index, M, K)
-    R, src = M, None
-    if src_rows is not None:
-        _require(src_rows.dim() == 1, f)
-        R = src_rows.shape[0]
-        src = _flat(src_rows, f, index, torch.int32, (R,))
-    if codes is None:
-        codes, ldq = _new((R, K), torch.int8, x.device, stream), K
-    else:
-        _require(codes.dtype is torch.int8, f)
-        ldq = _rows(codes, f, index, R, K)
-    if scales is None:
-        scales = _new((R,), torch.float32, x.device, stream)
-        sp = scales.data_ptr()
-    else:
-        sp = _flat(scales, f, index, torch.float32, (R,))
-    _call(index, stream, f, lib.moe_quantize_rows, x.data_ptr(), ldx, M, dtypes.get(x.dtype, -1), src, R, K,
-          codes.data_ptr(), ldq, sp)
-    return codes, scales
-
-
-def _product(f, x, w, offsets, out_dtype, out, stream):
-    """Checks of the grouped products and their common arguments."""
-    torch = _ENV[0]
-    if x.dim() != 2 or not x.is_cuda or w.dtype is not x.dtype or w.get_device() != x.get_device():
-        raise MoEError(1, f)
-    index = x.get_device()
-    R, K = x.shape
-    ldx = K if x.is_contiguous() else _rows(x, f, index, R, K)
-    shape, strides = w.shape, w.stride()
-    if len(shape) == 2:
-        E, N = 1, shape[0]
-        ldw, ldwe = strides[0], 0
-    else:
-        _require(len(shape) == 3, f)
-        E, N = shape[0], shape[1]
-        ldwe, ldw = strides[0], strides[1]
-    _require(shape[-1] == K and (strides[-1] == 1 or K == 1), f)
-    off = None
-    if offsets is not None:
-        off = _flat(offsets, f, index, torch.int32, (E + 1,))
-    if out is None:
-        out, ldy = _new((R, N), out_dtype, x.device, stream), N
-    else:
-        _require(out_dtype is None or out.dtype is out_dtype, f)
-        ldy = _rows(out, f, index, R, N)
-    return index, ldx, ldw, ldwe, off, R, E, K, N, out, ldy
+    return (_BINDING or _ops()).quantize_rows(x, src_rows, codes, scales, stream)
 
 
 def moe_int8_matmul(x, row_scales, w, channel_scales, offsets=None, out_dtype=None, out=None,
@@ -523,31 +366,14 @@ def moe_int8_matmul(x, row_scales, w, channel_scales, offsets=None, out_dtype=No
     [E, N]), e the expert whose range offsets[e] <= r < offsets[e + 1] holds r
     (int32 [E + 1] on the device; None: one matrix for all rows). Rows in no
     range are left as they were. out_dtype: bf16 (default), fp16 or fp32."""
-    torch, lib, codes = _ENV or _env()
-    f = "moe_int8_matmul"
-    _require(x.dtype is torch.int8, f)
-    if out is None and out_dtype is None:
-        out_dtype = torch.bfloat16
-    index, ldx, ldw, ldwe, off, R, E, K, N, out, ldy = _product(f, x, w, offsets, out_dtype, out, stream)
-    xs = _flat(row_scales, f, index, torch.float32, (R,))
-    ws = _flat(channel_scales, f, index, torch.float32, w.shape[:-1])
-    _call(index, stream, f, lib.moe_int8_matmul, x.data_ptr(), ldx, xs, w.data_ptr(), ldw, ldwe, ws, off, R, E, K, N,
-          out.data_ptr(), ldy, codes.get(out.dtype, -1))
-    return out
+    return (_BINDING or _ops()).int8_matmul(x, row_scales, w, channel_scales, offsets, out_dtype, out, stream)
 
 
 def moe_grouped_matmul(x, w, offsets=None, out_dtype=None, out=None, stream: Optional[int] = None):
     """y[r, n] = sum_k x[r, k] w[e, n, k] of bf16 or fp16 rows x [R, K] in expert
     order and experts w [E, N, K] (or [N, K]); offsets as for moe_int8_matmul.
     out_dtype: bf16, fp16 or fp32 (default: x's)."""
-    _, lib, codes = _ENV or _env()
-    f = "moe_grouped_matmul"
-    if out is None and out_dtype is None:
-        out_dtype = x.dtype
-    index, ldx, ldw, ldwe, off, R, E, K, N, out, ldy = _product(f, x, w, offsets, out_dtype, out, stream)
-    _call(index, stream, f, lib.moe_grouped_matmul, x.data_ptr(), ldx, w.data_ptr(), ldw, ldwe, off, R, E, K, N,
-          codes.get(x.dtype, -1), out.data_ptr(), ldy, codes.get(out.dtype, -1))
-    return out
+    return (_BINDING or _ops()).grouped_matmul(x, w, offsets, out_dtype, out, stream)
 
 
 def moe_op_sync_status(stream: Optional[int] = None) -> int:

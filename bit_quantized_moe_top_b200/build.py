@@ -1,4 +1,5 @@
-"""Build the in-tree CUDA library ``libmoeq.so`` for sm_100a with nvcc."""
+"""Build the in-tree CUDA library ``libmoeq.so`` for sm_100a with nvcc, and the
+binding of the operators to torch tensors with the host compiler."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -11,6 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmoeq.so")
+BINDING = os.path.join(HERE, "_binding.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["moe_layer.cu", "route.cu", "relayout.cu", "decode_gemm.cu", "lowrank.cu", "noalloc.cu", "prefill_gemm.cu",
@@ -34,16 +36,50 @@ def _inputs():
     return srcs, deps
 
 
+def _binding_inputs():
+    return [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "moe_layer.h")]
+
+
+def _newer(out, deps) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(d) <= os.path.getmtime(out) for d in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _inputs()[1])
+    return _newer(LIB, _inputs()[1]) and _newer(BINDING, _binding_inputs())
+
+
+def build_binding() -> str:
+    """The calls on torch tensors: host code against torch's headers, linked to libmoeq.so beside it."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+           "-I", os.path.join(ROOT, "include"), os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+           "-L", HERE, "-lmoeq", "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> str:
     if not force and up_to_date():
         return LIB
+    if force or not _newer(LIB, _inputs()[1]):
+        build_library(verbose, ptxas_v)
+    if force or not _newer(BINDING, _binding_inputs()):
+        build_binding()
+    return LIB
+
+
+def build_library(verbose: bool = False, ptxas_v: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs, _ = _inputs()
     cc = nvcc()

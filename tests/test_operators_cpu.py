@@ -164,21 +164,27 @@ def test_pointers_off_their_elements_are_refused(bq):
     assert lib.moe_int8_matmul(P, 64, P, P, 64, 0, P, None, 4, 1, 64, 32, P + 2, 32, bq.FP32, None) == INVALID
 
 
-def test_packed_norm_arguments_match_the_struct(bq):
-    """The binding packs moe_block_norm_t as bytes: same size and field offsets as the ctypes struct."""
-    import struct
-    assert bq._NORM_ARGS.size == ctypes.sizeof(bq.BlockNormArgs)
-    codes = {ctypes.c_int: "i", ctypes.c_void_p: "P", ctypes.c_longlong: "q", ctypes.c_float: "f"}
-    fmt = "@"
-    for name, typ in bq.BlockNormArgs._fields_:
-        fmt += codes[typ]
-        assert struct.calcsize(fmt) - struct.calcsize("@" + codes[typ]) == getattr(bq.BlockNormArgs, name).offset, name
-    assert fmt == bq._NORM_ARGS.format
-
-
 def test_product_extents(bq):
     lib = bq._lib()
     big = (1 << 29) + 1
     for rows, K, N in ((big, 64, 32), (4, big, 32), (4, 64, big)):
         assert lib.moe_grouped_matmul(P, K, P, K, 0, None, rows, 1, K, N, bq.BF16, P, N, bq.BF16, None) == TOO_LARGE
         assert lib.moe_int8_matmul(P, K, P, P, K, 0, P, None, rows, 1, K, N, P, N, bq.BF16, None) == TOO_LARGE
+
+
+def test_binding_refuses_without_a_device(bq):
+    """The calls on torch tensors take CUDA tensors only, name the call in their errors, and check their types."""
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for name, call in (("moe_block_norm", lambda: bq.moe_block_norm(x, x)),
+                       ("moe_block_norm", lambda: bq.moe_block_norm()),
+                       ("moe_quantize_rows", lambda: bq.moe_quantize_rows(x)),
+                       ("moe_int8_matmul", lambda: bq.moe_int8_matmul(x.to(torch.int8), torch.ones(4), x.to(torch.int8),
+                                                                      torch.ones(4))),
+                       ("moe_grouped_matmul", lambda: bq.moe_grouped_matmul(x, x))):
+        with pytest.raises(bq.MoEError, match=name) as ei:
+            call()
+        assert ei.value.status == INVALID
+    for call in (lambda: bq.moe_quantize_rows(3), lambda: bq.moe_block_norm("x"),
+                 lambda: bq.moe_grouped_matmul(None, x)):
+        with pytest.raises(TypeError):
+            call()
