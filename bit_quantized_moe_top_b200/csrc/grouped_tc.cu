@@ -21,7 +21,7 @@
 // of the cycles in 16 bits, 88% in 8, at the clock that the power limit leaves);
 // with some hundred rows per expert the reads of L2, which a tile of few rows
 // needs more of per MMA (32 experts of 384 rows: busy 75%); with a few rows per
-// expert the weights' bytes (64 rows in 8 experts of 4096 x 28672: 307 us, 95%
+// expert the weights' bytes (128 rows in 8 experts of 4096 x 28672: 307 us, 95%
 // of HBM's rate); with a few rows in all, latency (4.8 us for 2 rows).
 // Roles: warp 0 TMA producer, warp 1 MMA (of the pair's first CTA), warps 2-9
 // epilogue. Every mbarrier wait is bounded; one that runs out sets the status
