@@ -70,7 +70,6 @@ struct TcArgs {
   uint32_t idesc;      // without the N field
   int NF;              // channel tiles
   uint32_t nf_inv;     // 2^32 / NF, rounded down, + 1
-  int unit;            // step of a tile's rows
   int nmax;            // rows per tile
   int stages, bslot;   // ring depth, bytes of a stage's x part
   int S;               // CTAs splitting K (CG = 1)
@@ -194,6 +193,7 @@ struct Tile {
 // as many distinct weight rows as activation rows.
 template <int CG>
 __device__ __forceinline__ Tile tile_of(const GroupTable& g, const TcArgs& a, int i) {
+  constexpr int kUnit = 16 * CG;  // step of a tile's rows
   // i / NF by a product that is one too large at most
   auto by_nf = [&](int v) {
     const int q = a.NF == 1 ? v : (int)__umulhi((uint32_t)v, a.nf_inv);
@@ -208,11 +208,11 @@ __device__ __forceinline__ Tile tile_of(const GroupTable& g, const TcArgs& a, in
   const int f = bt == 1 ? in : in / bt, tk = band * kBandTc + in - f * bt;
   // widths in units that differ by one at most, so that no tile reads its
   // weights for a few rows only
-  const int units = (rows + a.unit - 1) / a.unit, base = nt == 1 ? units : units / nt, more = units - base * nt;
+  const int units = (rows + kUnit - 1) / kUnit, base = nt == 1 ? units : units / nt, more = units - base * nt;
   const int u0 = tk * base + min(tk, more);
-  t.n = (base + (tk < more ? 1 : 0)) * a.unit;
-  t.live = min(t.n, rows - u0 * a.unit);
-  t.r0 = g.begin[t.e] + u0 * a.unit;
+  t.n = (base + (tk < more ? 1 : 0)) * kUnit;
+  t.live = min(t.n, rows - u0 * kUnit);
+  t.r0 = g.begin[t.e] + u0 * kUnit;
   t.f0 = f * 128 * CG;
   return t;
 }
@@ -238,12 +238,13 @@ __device__ __forceinline__ bool piece_of(const GroupTable& g, const TcArgs& a, c
     t = tile_of<CG>(g, a, i);
     return true;
   }
+  constexpr int kUnit = 16 * CG;
   const int j = i - w.whole, shift = w.parts == 4 ? 2 : 1, p = j & (w.parts - 1);
   t = tile_of<CG>(g, a, w.whole + (j >> shift));
-  const int units = t.n / a.unit, u0 = units * p >> shift, u1 = units * (p + 1) >> shift;
-  t.n = (u1 - u0) * a.unit;
-  t.live = min(t.n, t.live - u0 * a.unit);
-  t.r0 += u0 * a.unit;
+  const int units = t.n / kUnit, u0 = units * p >> shift, u1 = units * (p + 1) >> shift;
+  t.n = (u1 - u0) * kUnit;
+  t.live = min(t.n, t.live - u0 * kUnit);
+  t.r0 += u0 * kUnit;
   return u1 > u0;
 }
 
@@ -779,7 +780,7 @@ cudaError_t launch_tc_typed(const TcArgs& a, int op, int y_dtype, int clusters, 
 }
 
 // what every form of the kernels needs; the instruction descriptor without its N field
-TcArgs common_args(const GroupedArgs& g, int op, int cg, int width, int unit) {
+TcArgs common_args(const GroupedArgs& g, int op, int cg, int width) {
   TcArgs a{};
   a.g = g;
   a.vec = reinterpret_cast<uintptr_t>(g.y) % 8 == 0 && g.ldy % 4 == 0;
@@ -788,8 +789,7 @@ TcArgs common_args(const GroupedArgs& g, int op, int cg, int width, int unit) {
   a.idesc |= (uint32_t)(128 * cg >> 4) << 24;
   a.NF = (g.N - 1) / (128 * cg) + 1;
   a.nf_inv = (uint32_t)((1ull << 32) / a.NF + 1);
-  a.unit = unit;
-  a.nmax = std::max(width, unit);
+  a.nmax = width;
   a.S = 1;
   return a;
 }
@@ -822,23 +822,28 @@ cudaError_t launch_grouped_tc(const GroupedArgs& g, int op, int y_dtype, cudaStr
   const long long ldx = g.rows > 1 ? g.ldx : (g.K + 15) / 16 * 16;
   const long long ldwe = g.E > 1 ? g.ldwe : g.ldw * g.N;
   const int nk = (g.K * es + kRowBytes - 1) / kRowBytes;
-  // Tile width and form. Groups are taken as equally large (their sizes are
-  // only known on the device). What a tile takes per 128 bytes of K is the
-  // larger of its MMAs, 2 cycles a row, and of the L2 reads of its CTA's 128
-  // channels and n / CG rows at about 55 bytes a cycle (measured: 8192 x 4096 x
-  // 4096 at 55, 12288 x 2048 x 2816 in 32 groups at 51), so narrower tiles cost
-  // nearly as much as wide ones, and it is the number of tiles that a CTA works
-  // off one after the other that counts. The split of K (CG = 1) pays an
-  // exchange of the partial sums, about 3500 cycles and 40 a column.
+  // Tile width and form, by an estimate of cycles. Groups are taken as equally
+  // large (their sizes are only known on the device). Per 128 bytes of K a CTA
+  // needs the larger of its MMAs, 2 cycles a row, and its L2 reads of 128
+  // channels and the rows it copies, at 60 bytes a cycle or its share of 6600 of
+  // all (8192 x 4096 x 4096 reads 12.5 TB/s). So narrower tiles cost nearly as
+  // much as wide ones, and it is the number of tiles that a CTA works off one
+  // after the other that counts. The split of K (CG = 1) pays an exchange of the
+  // partial sums, about 1500 cycles and 55 a column, a pair about 300 to set up.
+  // Clusters of eight are left out: not all of those that would fill the SMs find
+  // room at once (1 x 7168 x 2048 17.0 us, four 10.6). Over 38 sizes of 1 to 2000
+  // rows the choice took at most 10% more than the best of all forms, 2% on average.
   const int groups = std::min(g.rows, g.E), mean = (g.rows - 1) / groups + 1;
   const int nf[3] = {0, (g.N - 1) / 128 + 1, (g.N - 1) / 256 + 1};  // channel tiles by CG
   const double streamed = (double)groups * g.N * nk * (kRowBytes / 3500.0);  // weights at HBM's bytes per cycle
   auto cost_of = [&](int cg, int width, int S) {
-    const int nt = (mean - 1) / width + 1, unit = cg == 2 || S == 8 ? 32 : 16;
+    const int nt = (mean - 1) / width + 1, unit = 16 * cg;
     const int n = ((mean - 1) / nt / unit + 1) * unit;
-    const int waves = (groups * nt * nf[cg] - 1) / (cg == 2 ? pairs : sms / S) + 1;
-    const double per_k = std::max(2.0 * n, (128 + n / cg) * (kRowBytes / 55.0));
-    return std::max(waves * per_k * ((nk - 1) / S + 1), streamed) + (S > 1 ? 3500 + 40 * n : 0);
+    const int tiles = groups * nt * nf[cg], slots = cg == 2 ? pairs : sms / S, waves = (tiles - 1) / slots + 1;
+    const double rate = std::min(60.0, 6600.0 / (cg * S * std::min(tiles, slots)));
+    const int loaded = (n / cg + kBoxRows - 1) / kBoxRows * kBoxRows;
+    const double per_k = std::max(2.0 * n, (128 + loaded) * kRowBytes / rate) + 0.1 * n;  // fewer MMAs where reads bound both
+    return std::max(waves * per_k * ((nk - 1) / S + 1), streamed) + (S > 1 ? 1500 + 55 * n : 0) + (cg == 2 ? 300 : 0);
   };
   int cg = 2, width = 256, S = 1;
   double best = cost_of(2, 256, 1);
@@ -857,10 +862,10 @@ cudaError_t launch_grouped_tc(const GroupedArgs& g, int op, int y_dtype, cudaStr
   for (int w = 128; w >= 16; w /= 2) {
     if (mean <= w / 2 && w > 16) continue;
     const int tiles = groups * nf[1] * ((mean - 1) / w + 1);
-    for (int s = 1; s <= 8 && tiles * s <= sms; s *= 2)
+    for (int s = 1; s <= 4 && tiles * s <= sms; s *= 2)
       if (s == 1 || nk >= s * 2) consider(1, w, s);
   }
-  TcArgs a = common_args(g, op, cg, width, cg == 2 || S == 8 ? 32 : 16);
+  TcArgs a = common_args(g, op, cg, width);
   a.S = S;
   const long long most = most_tiles(g, a.nmax, a.NF);
   if (!encode_rows(&a.map_w, g.w, op, es, g.K, g.N, g.ldw, g.E, ldwe, 128)) return cudaErrorInvalidValue;
@@ -884,7 +889,7 @@ cudaError_t launch_grouped_loads(const GroupedArgs& g, int op, int y_dtype, cuda
   const int NF = (g.N - 1) / 128 + 1;
   int width = 128;  // narrower only where there would not be a tile for every SM
   while (width > 16 && most_tiles(g, width, NF) < device_sms()) width /= 2;
-  const TcArgs a = common_args(g, op, 1, width, 16);
+  const TcArgs a = common_args(g, op, 1, width);
   const int grid = (int)std::min<long long>(most_tiles(g, width, NF), 2LL * device_sms());
   return by_types(op, y_dtype, [&](auto i8, auto out) {
     return launch_loads<decltype(i8)::value, decltype(out)>(a, grid, st);
