@@ -155,7 +155,7 @@ template <typename T, bool SHIFT>
 __device__ __forceinline__ void store8(T* row, int e, int K, const float2 (&f)[4]) {
   T* p = row + e;
   if (!SHIFT || (e >= 0 && e + 8 <= K && (reinterpret_cast<uintptr_t>(p) & 15) == 0)) {
-    store_vec<T, 8>(p, reinterpret_cast<const float*>(f));
+    store_vec<T>(p, reinterpret_cast<const float*>(f));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
