@@ -144,6 +144,39 @@ __device__ __forceinline__ void build_group_table(GroupTable& g, const int* offs
     __syncthreads();
     return;
   }
+  if (E <= 32) {  // one warp, without the passes between warps
+    if (warp == 0) {
+      int lo = 0, hi = 0;
+      if (lane < E) {
+        lo = min(max(offsets[lane], 0), rows);
+        hi = min(max(offsets[lane + 1], 0), rows);
+      }
+      int m = max(lo, hi);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, m, d);
+        if (lane >= d) m = max(m, o);
+      }
+      const int prev = __shfl_up_sync(0xffffffffu, m, 1);
+      const int start = lane == 0 ? lo : max(lo, prev);
+      const int n = lane < E ? m - start : 0;
+      int s = n > 0 ? tiles_of(n) : 0;
+      const int own = s;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += o;
+      }
+      if (lane < E) {
+        g.begin[lane] = start;
+        g.rows[lane] = n;
+        g.first[lane] = s - own;
+        if (lane == E - 1) g.first[E] = s;
+      }
+    }
+    __syncthreads();
+    return;
+  }
   int lo = 0, hi = 0;
   if (t < E) {
     lo = min(max(offsets[t], 0), rows);
@@ -159,7 +192,11 @@ __device__ __forceinline__ void build_group_table(GroupTable& g, const int* offs
   if (t < kMaxExperts && lane == 31) g.scratch[0][warp] = m;
   __syncthreads();
   int before = 0;
-  for (int w = 0; w < min(warp, kMaxExperts / 32); ++w) before = max(before, g.scratch[0][w]);
+#pragma unroll
+  for (int w = 0; w < kMaxExperts / 32; ++w) {
+    const int o = g.scratch[0][w];
+    if (w < warp) before = max(before, o);
+  }
   int prev = __shfl_up_sync(0xffffffffu, m, 1);
   prev = lane == 0 ? before : max(prev, before);
   m = max(m, before);
@@ -175,7 +212,11 @@ __device__ __forceinline__ void build_group_table(GroupTable& g, const int* offs
   if (t < kMaxExperts && lane == 31) g.scratch[1][warp] = s;
   __syncthreads();
   int base = 0;
-  for (int w = 0; w < min(warp, kMaxExperts / 32); ++w) base += g.scratch[1][w];
+#pragma unroll
+  for (int w = 0; w < kMaxExperts / 32; ++w) {
+    const int o = g.scratch[1][w];
+    if (w < warp) base += o;
+  }
   if (t < E) {
     g.begin[t] = start;
     g.rows[t] = n;
