@@ -177,7 +177,10 @@ __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const _
         uint32_t v[32];
         tmem_ld32_nw(tmem + ((uint32_t)(quarter * 32) << 16) + c0, v);
         tmem_wait_ld(v);
-        store_chunk<TO, I8>(a, t, c0, v, ws, stage, xs_s[warp], ch0, lane, kSumChunks<I8, TO> && first > 0);
+        float xv = 0.f;
+        if constexpr (I8)
+          if (c0 + lane < t.live) xv = a.g.xs[t.r0 + c0 + lane];
+        store_chunk<TO, I8>(a, t, c0, v, ws, xv, stage, xs_s[warp], ch0, lane, kSumChunks<I8, TO> && first > 0);
       }
       tc_fence_before();
       __syncwarp();

@@ -277,12 +277,13 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
 // cross the warp's 2 KiB of shared memory as pairs of rows, so that a store
 // covers four rows of 32 channels, 8 bytes a lane; 32-bit outputs go out
 // directly, one row of 32 channels per store, or are added to what is there.
+// ws: the lane's channel's scale, xv: the scale of row c0 + lane.
 template <typename TO, bool I8>
 __device__ __forceinline__ void store_chunk(const TcArgs& a, const Tile& t, int c0, const uint32_t (&v)[32], float ws,
-                                            uint32_t* stage, float* xs, int ch0, int lane, bool add = false) {
+                                            float xv, uint32_t* stage, float* xs, int ch0, int lane, bool add = false) {
   float sc[32];
   if constexpr (I8) {
-    xs[lane] = c0 + lane < t.live ? a.g.xs[t.r0 + c0 + lane] : 0.f;
+    xs[lane] = xv;
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
@@ -501,10 +502,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
     }
   } else {
     // two warps per 32 channels, taking the tile's column chunks in turn
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int quarter = warp & 3;
     uint32_t* stage = reinterpret_cast<uint32_t*>(tail) + (warp - 2) * 512;
     float* xs = xs_s[warp - 2];
-    int u = 0;
+    int u = 0, it = 0;
     auto filled = [&](int buf) {
       const bool ok = role_wait(acc_full(buf), (u >> 1) & 1, status, a.g.wait_ns, aborted);
       return __all_sync(0xffffffffu, ok);
@@ -520,6 +521,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
     for (int i = cluster; i < work.items; i += nclusters) {
       Tile t;
       if (!piece_of<CG>(g, a, work, i, t)) continue;
+      // tiles of up to 32 rows go to one half of the warps, in turn
+      const int half = ((warp - 2) >> 2) ^ (it++ & 1);
       const int ch0 = t.f0 + (CG == 2 ? (int)rank * 128 : 0) + quarter * 32, ch = ch0 + lane;
       const bool split = CG == 1 && a.S > 1;
       // Of a split tile the partial sums of columns [q c, q c + c) go to CTA q,
@@ -531,9 +534,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
         const int q = col / c;
         st_cluster_v4(map_rank(part + (uint32_t)(col - q * c) * 512, q), v);
       };
+      // scales are on their way while the accumulators are filled
       float ws = 0.f;
+      auto row_scale = [&](int c0) {
+        float x = 0.f;
+        if constexpr (I8)
+          if (c0 + lane < t.live) x = a.g.xs[t.r0 + c0 + lane];
+        return x;
+      };
       if constexpr (I8)
         if (ch < a.g.N) ws = a.g.ws[(long long)t.e * a.g.N + ch];
+      float xv = split ? 0.f : row_scale(half * 32);
       bool ok = true;
       if constexpr (kSum) {
         constexpr int kParts = kUnitCols / 64;
@@ -571,7 +582,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
               for (int j = 0; j < 32; j += 4)
                 if (c0 + j < t.n) send(c0 + j, sum[p] + j);
             } else {
-              store_chunk<TO, I8>(a, t, c0, sum[p], ws, stage, xs, ch0, lane);
+              store_chunk<TO, I8>(a, t, c0, sum[p], ws, 0.f, stage, xs, ch0, lane);
             }
           }
         }
@@ -590,11 +601,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
             for (int c0 = c_first; c0 < t.n; c0 += 128) {
               tmem_wait_ld(v[0]);
               if (c0 + 64 < t.n) tmem_ld32_nw(d + c0 + 64, v[1]);
-              store_chunk<TO, I8>(a, t, c0, v[0], ws, stage, xs, ch0, lane);
+              float xn = row_scale(c0 + 64);
+              store_chunk<TO, I8>(a, t, c0, v[0], ws, xv, stage, xs, ch0, lane);
               if (c0 + 64 < t.n) {
                 tmem_wait_ld(v[1]);
                 if (c0 + 128 < t.n) tmem_ld32_nw(d + c0 + 128, v[0]);
-                store_chunk<TO, I8>(a, t, c0 + 64, v[1], ws, stage, xs, ch0, lane);
+                xv = row_scale(c0 + 128);
+                store_chunk<TO, I8>(a, t, c0 + 64, v[1], ws, xn, stage, xs, ch0, lane);
               }
             }
           } else {

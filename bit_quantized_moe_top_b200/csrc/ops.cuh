@@ -225,14 +225,16 @@ __device__ __forceinline__ void build_group_table(GroupTable& g, const int* offs
   }
   __syncthreads();
 }
-// the expert whose tiles hold tile i (first[e] <= i < first[e + 1])
+// The expert whose tiles hold tile i (first[e] <= i < first[e + 1]): the last
+// one that begins no later, counted by a whole warp, 8 experts a lane and then
+// those one by one.
 __device__ __forceinline__ int find_group(const GroupTable& g, int E, int i) {
-  int lo = 0, hi = E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (g.first[mid] <= i) lo = mid; else hi = mid - 1;
-  }
-  return lo;
+  static_assert(kMaxExperts <= 256, "two steps of 32 and 8");
+  const int lane = threadIdx.x & 31;
+  int from = 0;
+  if (E > 32) from = 8 * (__popc(__ballot_sync(0xffffffffu, lane * 8 < E && g.first[min(lane * 8, E)] <= i)) - 1);
+  const int e = from + lane;
+  return from + __popc(__ballot_sync(0xffffffffu, e < E && g.first[min(e, E)] <= i)) - 1;
 }
 
 }  // namespace moeq
