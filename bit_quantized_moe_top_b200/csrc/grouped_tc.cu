@@ -22,7 +22,7 @@
 // with some hundred rows per expert the reads of L2, which a tile of few rows
 // needs more of per MMA (32 experts of 384 rows: busy 75%); with a few rows per
 // expert the weights' bytes (128 rows in 8 experts of 4096 x 28672: 307 us, 95%
-// of HBM's rate); with a few rows in all, latency (4.8 us for 2 rows).
+// of HBM's rate); with a few rows in all, latency (4.3 us for 2 rows).
 // Roles: warp 0 TMA producer, warp 1 MMA (of the pair's first CTA), warps 2-9
 // epilogue. Every mbarrier wait is bounded; one that runs out sets the status
 // word, every role of the CTA stops at its next wait, the cluster drains its
@@ -405,8 +405,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
       if (b * kBoxRows * CG < a.nmax) prefetch_map(&a.map_x[b]);
   }
   if (warp == 1) alloc_tmem<CG>(smem_u32(&tmem_slot), kCols);
+  auto sync = [&] {
+    if (csize > 1) cluster_sync();
+    else __syncthreads();
+  };
   tc_fence_before();
-  cluster_sync();
+  sync();
   tc_fence_after();
   pdl_wait();  // what precedes touches no memory of the call
   pdl_trigger();
@@ -679,7 +683,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
   if (threadIdx.x == 0 && abort_s)
     for (int q = 0; q < csize; ++q) st_cluster_u32(map_rank(smem_u32(&cluster_abort), q), 1u);
   tc_fence_before();
-  cluster_sync();
+  sync();
   tc_fence_after();
   if (*(volatile uint32_t*)&cluster_abort) {
     // Wait for every copy in flight. Where one CTA of a pair filled a stage and
