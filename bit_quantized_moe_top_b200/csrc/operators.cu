@@ -15,7 +15,8 @@ std::atomic<unsigned long long> g_wait_ns{kDefaultWaitNs};
 bool is16(int d) { return d == MOE_BF16 || d == MOE_FP16; }
 bool is_out(int d) { return is16(d) || d == MOE_FP32; }
 
-constexpr int kMaxExtent = 1 << 29;  // of the products' sizes: coordinates and K in bytes stay within an int
+constexpr int kMaxExtent = 1 << 29;  // rows and N: coordinates stay within an int
+constexpr int kMaxSum = 1 << 24;     // K: a tile's sums take far less than the limit of the waits for them
 
 // whether a pointer lies at a multiple of its elements' size
 bool at_elements(const void* p, int es) { return reinterpret_cast<uintptr_t>(p) % es == 0; }
@@ -27,7 +28,7 @@ moe_status_t check_product(const void* x, long long ldx, const void* w, long lon
                            int es, const int* offsets, int rows, int E, int K, int N, const void* y, long long ldy,
                            int yd) {
   if (rows < 0 || E < 1 || K < 1 || N < 1 || !is_out(yd)) return MOE_ERR_INVALID_ARG;
-  if (E > kMaxExperts || rows > kMaxExtent || K > kMaxExtent || N > kMaxExtent) return MOE_ERR_TOO_LARGE;
+  if (E > kMaxExperts || rows > kMaxExtent || K > kMaxSum || N > kMaxExtent) return MOE_ERR_TOO_LARGE;
   if (!offsets && E != 1) return MOE_ERR_INVALID_ARG;
   if (ldx < 0 || ldw < 0 || ldwe < 0 || (rows > 1 && ldy < N)) return MOE_ERR_INVALID_ARG;
   if (rows > 0 && (!x || !w || !y)) return MOE_ERR_INVALID_ARG;

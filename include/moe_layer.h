@@ -396,8 +396,8 @@ moe_status_t moe_quantize_rows(const void* x, long long x_stride, int x_rows, mo
  * they were. Offsets that descend or leave the range are read as their running
  * maximum clamped to [0, rows].
  * x int8 [rows, K], w int8 [experts, N, K], channel_scales fp32 [experts, N],
- * y [rows, N] of y_dtype. K <= 131071 (int32 sums), experts <= 256, rows, N and
- * K <= 2^29, else MOE_ERR_TOO_LARGE. Pointers and strides of x and w that are not multiples of
+ * y [rows, N] of y_dtype. K <= 131071 (int32 sums), experts <= 256, rows and
+ * N <= 2^29, else MOE_ERR_TOO_LARGE. Pointers and strides of x and w that are not multiples of
  * 16 bytes, and rows that overlap, which bulk copies cannot address, take a
  * kernel with ordinary loads, four to seven times slower. */
 moe_status_t moe_int8_matmul(const signed char* x, long long x_stride, const float* row_scales, const signed char* w,
@@ -408,7 +408,7 @@ moe_status_t moe_int8_matmul(const signed char* x, long long x_stride, const flo
 /* The same grouped by expert for 16-bit experts: y[r, n] = sum_k x[r, k] *
  * w[e, n, k], fp32 sums, rounded once to y_dtype. (The tensor cores' sums
  * truncate; an fp32 y adds them up every 512 values of K, rounded to nearest.) x and w share dtype (MOE_BF16
- * or MOE_FP16). offsets, limits (experts) and strides as above. */
+ * or MOE_FP16). K <= 2^24; offsets, other limits and strides as above. */
 moe_status_t moe_grouped_matmul(const void* x, long long x_stride, const void* w, long long w_stride,
                                 long long expert_stride, const int* offsets, int rows, int experts, int K, int N,
                                 moe_dtype_t dtype, void* y, long long y_stride, moe_dtype_t y_dtype,

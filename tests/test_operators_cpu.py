@@ -167,7 +167,7 @@ def test_pointers_off_their_elements_are_refused(bq):
 def test_product_extents(bq):
     lib = bq._lib()
     big = (1 << 29) + 1
-    for rows, K, N in ((big, 64, 32), (4, big, 32), (4, 64, big)):
+    for rows, K, N in ((big, 64, 32), (4, (1 << 24) + 1, 32), (4, 64, big)):
         assert lib.moe_grouped_matmul(P, K, P, K, 0, None, rows, 1, K, N, bq.BF16, P, N, bq.BF16, None) == TOO_LARGE
         assert lib.moe_int8_matmul(P, K, P, P, K, 0, P, None, rows, 1, K, N, P, N, bq.BF16, None) == TOO_LARGE
 
