@@ -2,18 +2,21 @@
 // strides that are not multiples of 16 bytes, rows that overlap. Included by
 // grouped_tc.cu, whose tiles, MMAs and stores it shares; only the copies differ.
 //
-// One CTA per 128 channels x up to 128 rows, two CTAs per SM. Eight warps load a
-// stage with ordinary loads, 16 bytes of a row at a time, write it to shared
+// One CTA per 128 channels x up to 128 rows, two CTAs per SM. Its eight warps load
+// a stage with ordinary loads, 16 bytes of a row at a time, write it to shared
 // memory in the swizzled layout that the MMAs read, and store the finished tile;
-// a ninth issues the MMAs. 16 bytes that lie across an aligned boundary are
-// shifted out of the two aligned pieces around them, or read element by element
-// where those would leave the row. Bound by the loads' latency, which two CTAs
-// of three stages cover in part: 16384 rows by 4096 channels of 14335 in 8
-// experts 7.6 ms (bulk copies at 14336: 1.27), 8-bit 3.9 (0.60); one row of 2047
-// by 2816 channels 44 us, 8-bit 29.
+// warp 0 issues the MMAs of a stage while the loads of the next are under way (a
+// warp of its own for them would leave the others 96 registers instead of 128, too
+// few for the loads of a stage beside the sums of the chunks: 25% slower).
+// 16 bytes that lie across an aligned boundary are shifted out of the two aligned
+// pieces around them, or read element by element where those would leave the row.
+// A tile's sums of earlier chunks wait in TMEM, beside the accumulators. Bound by
+// the loads' latency, which two CTAs of three stages cover in part: 16384 rows by
+// 4096 channels of 14335 in 8 experts 7.8 ms (bulk copies at 14336: 1.38), 8-bit
+// 4.0 (0.65); one row of 2047 by 2816 channels 47 us, 8-bit 29.
 
 constexpr int kLoadWarps = 8;
-constexpr int kThreadsLoads = 32 * (kLoadWarps + 1);
+constexpr int kThreadsLoads = 32 * kLoadWarps;
 constexpr int kStagesLoads = 3;
 
 // Bytes b .. b + 15 of a row of len bytes, as loaded
@@ -21,7 +24,7 @@ template <int ES>
 struct Chunk16 {
   uint32_t w[8];
   int mis;  // 0, or the offset within the two pieces
-  __device__ __forceinline__ void load(const uint8_t* row, long long b, long long len, bool have) {
+  __device__ __forceinline__ void load(const uint8_t* row, int b, int len, bool have) {
     mis = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = 0;
@@ -63,24 +66,6 @@ struct Chunk16 {
   }
 };
 
-// A CTA's work in the order in which it is done: its tiles, whole or, where sums
-// are taken in chunks, a chunk of K at a time (added up in y).
-template <bool CHUNKS>
-struct PartOf {
-  int tile, first, end, total, nk;
-  __device__ __forceinline__ PartOf(int total_, int nk_)
-      : tile((int)blockIdx.x - (int)gridDim.x), first(nk_), end(nk_), total(total_), nk(nk_) {}
-  __device__ __forceinline__ bool next(bool ok) {
-    first = end;
-    if (first >= nk) {
-      first = 0;
-      tile += gridDim.x;
-    }
-    end = CHUNKS ? min(first + kChunk, nk) : nk;
-    return ok && tile < total;
-  }
-};
-
 template <bool I8, typename TO>
 __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const __grid_constant__ TcArgs a) {
   extern __shared__ uint8_t raw[];
@@ -90,8 +75,8 @@ __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const _
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
   constexpr int ES = I8 ? 1 : 2;
-  constexpr uint32_t kCols = 128;
-  using Part = PartOf<kSumChunks<I8, TO>>;
+  constexpr uint32_t kSums = 128;  // first TMEM column of the sums of a tile's earlier chunks
+  constexpr uint32_t kCols = I8 ? kSums : 2 * kSums;
   constexpr int kStage = kABytes + 128 * kRowBytes;
   const uint32_t pad = (1024u - (smem_u32(raw) & 1023u)) & 1023u;
   uint8_t* sm = raw + pad;
@@ -113,7 +98,7 @@ __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const _
     abort_s = 0;
     fence_barrier_init();
   }
-  if (warp == kLoadWarps) tmem_alloc(smem_u32(&tmem_slot), kCols);
+  if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -122,33 +107,68 @@ __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const _
   build_group_table(g, a.g.offsets, a.g.rows, a.g.E, RowTilesTc{a.nmax});
   const uint32_t tmem = tmem_slot;
   const int total = g.first[a.g.E] * a.NF;
-  const long long len = (long long)a.g.K * ES;
-  const int nk = (int)((len + kRowBytes - 1) / kRowBytes);
+  const int len = a.g.K * ES, nk = (len + kRowBytes - 1) / kRowBytes;
 
-  if (warp < kLoadWarps) {
-    const int quarter = warp & 3, half = warp >> 2;
-    const int lr = threadIdx.x >> 3, lc = threadIdx.x & 7;  // this thread's row (+ 32 j) and 16 bytes of a stage
-    const uint32_t place = (uint32_t)(lr * kRowBytes + ((lc ^ (lr & 7)) << 4));
-    // the stages are free while a tile is stored: all its MMAs are done and the next is not begun
-    uint32_t* stage = reinterpret_cast<uint32_t*>(sm) + warp * 512;
-    int slot = 0, round = 0, it = 0;
-    bool ok = true;
-    for (Part q(total, nk); q.next(ok); ++it) {
-      const int first = q.first, end = q.end;
-      const Tile t = tile_of<1>(g, a, q.tile);
-      const uint8_t* x = static_cast<const uint8_t*>(a.g.x) + (long long)t.r0 * a.g.ldx * ES;
-      const uint8_t* w = static_cast<const uint8_t*>(a.g.w) + ((long long)t.e * a.g.ldwe + (long long)t.f0 * a.g.ldw) * ES;
-      for (int kb = first; kb < end; ++kb) {
-        const long long b = (long long)kb * kRowBytes + lc * 16;
+  const int quarter = warp & 3, half = warp >> 2;
+  const int lr = threadIdx.x >> 3, lc = threadIdx.x & 7;  // this thread's row (+ 32 j) and 16 bytes of a stage
+  const uint32_t place = (uint32_t)(lr * kRowBytes + ((lc ^ (lr & 7)) << 4));
+  // the stages are free while a tile is stored: all its MMAs are done and the next is not begun
+  uint32_t* stage = reinterpret_cast<uint32_t*>(sm) + warp * 512;
+  const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16);
+  int slot = 0, round = 0, it = 0;  // it: accumulators filled so far
+  int mslot = 0, mph = 0;           // of the next MMAs (warp 0)
+  bool ok = true;
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    const bool done = role_wait(bar, parity, status, a.g.wait_ns, aborted);
+    return (bool)__all_sync(0xffffffffu, done);
+  };
+  // the MMAs of one stage, once every warp has written its part
+  auto issue = [&](uint32_t idesc, bool first, bool last) {
+    ok = wait(full(mslot), mph);
+    if (!ok) return;
+    tc_fence_after();
+    if (elect_one()) {
+      const uint64_t ad = sw128_desc(sbase + mslot * kStage), bd = sw128_desc(sbase + mslot * kStage + kABytes);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mma_ss<1, I8>(tmem, ad + 2 * k, bd + 2 * k, idesc, !first || k > 0);
+      commit<1>(empty(mslot));
+      if (last) commit<1>(acc_full);
+    }
+    __syncwarp();
+    if (++mslot == kStagesLoads) {
+      mslot = 0;
+      mph ^= 1;
+    }
+  };
+  for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+    const Tile t = tile_of<1>(g, a, i);
+    const uint8_t* x = static_cast<const uint8_t*>(a.g.x) + (long long)t.r0 * a.g.ldx * ES;
+    const uint8_t* w = static_cast<const uint8_t*>(a.g.w) + ((long long)t.e * a.g.ldwe + (long long)t.f0 * a.g.ldw) * ES;
+    const uint8_t *wr[4], *xr[4];  // this thread's rows
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      wr[j] = w + (long long)(lr + 32 * j) * a.g.ldw * ES;
+      xr[j] = x + (long long)(lr + 32 * j) * a.g.ldx * ES;
+    }
+    const uint32_t idesc = a.idesc | ((uint32_t)(t.n >> 3) << 17);
+    for (int kb = 0; kb < nk && ok; ++it) {
+      const int first = I8 ? 0 : kb, end = I8 ? nk : min(kb + kChunk<TO>, nk);
+      for (; kb < end; ++kb) {
+        const int b = kb * kRowBytes + lc * 16;
         Chunk16<ES> cw[4], cx[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int r = lr + 32 * j;
-          cw[j].load(w + (long long)r * a.g.ldw * ES, b, len, t.f0 + r < a.g.N);
-          cx[j].load(x + (long long)r * a.g.ldx * ES, b, len, r < t.live);
+          cw[j].load(wr[j], b, len, t.f0 + r < a.g.N);
+          cx[j].load(xr[j], b, len, r < t.live);
         }
-        ok = round == 0 || role_wait(empty(slot), (round - 1) & 1, status, a.g.wait_ns, aborted);
-        ok = __all_sync(0xffffffffu, ok);
+        // under the loads' latency the stage before this one
+        if (warp == 0 && kb > first) {
+          if (kb == first + 1 && it > 0) ok = wait(acc_empty, (it - 1) & 1);
+          if (ok) issue(idesc, kb == first + 1, false);
+          if (!ok) break;
+        }
+        ok = round == 0 || wait(empty(slot), (round - 1) & 1);
         if (!ok) break;
         uint8_t* dst = sm + slot * kStage + place;
 #pragma unroll
@@ -165,61 +185,47 @@ __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const _
         }
       }
       if (!ok) break;
+      if (warp == 0) {
+        if (end == first + 1 && it > 0) ok = wait(acc_empty, (it - 1) & 1);
+        if (ok) issue(idesc, end == first + 1, true);
+        if (!ok) break;
+      }
       const int ch0 = t.f0 + quarter * 32;
       float ws = 0.f;
       if constexpr (I8)
         if (ch0 + lane < a.g.N) ws = a.g.ws[(long long)t.e * a.g.N + ch0 + lane];
-      ok = role_wait(acc_full, it & 1, status, a.g.wait_ns, aborted);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = wait(acc_full, it & 1);
       if (!ok) break;
       tc_fence_after();
       for (int c0 = half * 32; c0 < t.n; c0 += 64) {
         uint32_t v[32];
-        tmem_ld32_nw(tmem + ((uint32_t)(quarter * 32) << 16) + c0, v);
+        tmem_ld32_nw(acc + c0, v);
         tmem_wait_ld(v);
+        if (!I8 && first > 0) {
+          uint32_t sum[32];
+          tmem_ld32_nw(acc + kSums + c0, sum);
+          tmem_wait_ld(sum);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(sum[j]) + __uint_as_float(v[j]));
+        }
+        if (!I8 && end < nk) {
+          tmem_st32(acc + kSums + c0, v);
+          continue;
+        }
         float xv = 0.f;
         if constexpr (I8)
           if (c0 + lane < t.live) xv = a.g.xs[t.r0 + c0 + lane];
-        store_chunk<TO, I8>(a, t, c0, v, ws, xv, stage, xs_s[warp], ch0, lane, kSumChunks<I8, TO> && first > 0);
+        store_chunk<TO, I8>(a, t, c0, v, ws, xv, stage, xs_s[warp], ch0, lane);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty);
-      ok = role_wait(acc_empty, it & 1, status, a.g.wait_ns, aborted);
-      ok = __all_sync(0xffffffffu, ok);
+      // no stage is written before every warp's part of a tile has left it
+      if (end == nk) ok = wait(acc_empty, it & 1);
     }
-    if (!ok) *aborted = 1;
-  } else {
-    int slot = 0, ph = 0, it = 0;
-    bool ok = true;
-    for (Part q(total, nk); q.next(ok); ++it) {
-      const int first = q.first, end = q.end;
-      const Tile t = tile_of<1>(g, a, q.tile);
-      ok = it == 0 || role_wait(acc_empty, (it - 1) & 1, status, a.g.wait_ns, aborted);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t idesc = a.idesc | ((uint32_t)(t.n >> 3) << 17);
-      for (int kb = first; kb < end; ++kb) {
-        ok = role_wait(full(slot), ph, status, a.g.wait_ns, aborted);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t ad = sw128_desc(sbase + slot * kStage), bd = sw128_desc(sbase + slot * kStage + kABytes);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mma_ss<1, I8>(tmem, ad + 2 * k, bd + 2 * k, idesc, kb > first || k > 0);
-          commit<1>(empty(slot));
-          if (kb == end - 1) commit<1>(acc_full);
-        }
-        __syncwarp();
-        if (++slot == kStagesLoads) {
-          slot = 0;
-          ph ^= 1;
-        }
-      }
-    }
-    if (!ok) *aborted = 1;
+  }
+  if (!ok) *aborted = 1;
+  if (warp == 0) {
     if (elect_one()) mma_commit(drained);
     __syncwarp();
     mbar_wait(drained, 0, status, kDrainLimitNs);
@@ -227,5 +233,5 @@ __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const _
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kLoadWarps) tmem_dealloc(tmem, kCols);
+  if (warp == 0) tmem_dealloc(tmem, kCols);
 }

@@ -54,14 +54,17 @@ constexpr int kBandTc = 8;                     // row tiles that share a sweep o
 constexpr int kStagingBytes = kEpiWarps * 2048;
 
 // The tensor cores add to their fp32 accumulators with truncation, whose error
-// grows with the number of additions: relative to the output 2.5e-6 over K =
-// 2048, four times that over 8192, where sums rounded to nearest stay at 1e-6.
-// A 16-bit output's own rounding hides that; for fp32 outputs the accumulators
-// are emptied every kChunk stages (512 values of K) and added up in fp32
-// registers, rounded to nearest: 6.5e-7 at any K.
-constexpr int kChunk = 8;
-template <bool I8, typename TO>
-constexpr bool kSumChunks = !I8 && sizeof(TO) == 4;
+// grows in proportion to the number of additions: relative to the output 6e-7
+// over 512 values of K summed in one go, 1.2e-6 over 1024, 2.5e-6 over 2048
+// (fp16; bf16 a fifth less), always towards zero. So the accumulators of 16-bit
+// operands are emptied every kChunk stages and added up in fp32, rounded to
+// nearest: 512 values for fp32 outputs, 1024 for 16-bit ones, whose own rounding
+// is far coarser (8192 x 4096 x 8192 in bf16: 341 us in one go, 347 with 1024
+// values, 351 with 512; misrounded outputs at K = 14336 0.8%, 0.07%, 0.04%,
+// nearest-rounded sums 0.08%). What remains to grow with K are the roundings to
+// nearest of K / 512 or K / 1024 additions: 7.7e-7 and 1.3e-6 at K = 2^20.
+template <typename TO>
+constexpr int kChunk = sizeof(TO) == 4 ? 8 : 16;
 
 struct TcArgs {
   CUtensorMap map_w;   // [E][N][K], box 128 rows
@@ -276,11 +279,11 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
 // One warp's 32 channels (lane = channel) of 32 rows to y. 16-bit outputs
 // cross the warp's 2 KiB of shared memory as pairs of rows, so that a store
 // covers four rows of 32 channels, 8 bytes a lane; 32-bit outputs go out
-// directly, one row of 32 channels per store, or are added to what is there.
+// directly, one row of 32 channels per store.
 // ws: the lane's channel's scale, xv: the scale of row c0 + lane.
 template <typename TO, bool I8>
 __device__ __forceinline__ void store_chunk(const TcArgs& a, const Tile& t, int c0, const uint32_t (&v)[32], float ws,
-                                            float xv, uint32_t* stage, float* xs, int ch0, int lane, bool add = false) {
+                                            float xv, uint32_t* stage, float* xs, int ch0, int lane) {
   float sc[32];
   if constexpr (I8) {
     xs[lane] = xv;
@@ -298,11 +301,7 @@ __device__ __forceinline__ void store_chunk(const TcArgs& a, const Tile& t, int 
   if constexpr (sizeof(TO) == 4) {
     if (ch0 + lane < a.g.N) {
       float* y = static_cast<float*>(a.g.y) + (long long)(t.r0 + c0) * a.g.ldy + ch0 + lane;
-      if (add) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j < rows) y[j * a.g.ldy] += scaled<I8>(v[j], I8 ? sc[j] : 0.f);
-      } else if (rows >= 32) {
+      if (rows >= 32) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) y[j * a.g.ldy] = scaled<I8>(v[j], I8 ? sc[j] : 0.f);
       } else {
@@ -362,7 +361,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
   constexpr int kUnitCols = CG == 2 ? 256 : 128;  // TMEM columns of one accumulator
   constexpr uint32_t kCols = 2 * kUnitCols;
   constexpr int kElem = I8 ? 128 : 64;            // elements per 128-byte row
-  constexpr bool kSum = kSumChunks<I8, TO>;
   const uint32_t pad = (1024u - (smem_u32(raw) & 1023u)) & 1023u;
   uint8_t* sm = raw + pad;
   const uint32_t sbase = smem_u32(sm);
@@ -468,7 +466,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
         if (!piece_of<CG>(g, a, work, i, t)) continue;
         const uint32_t idesc = a.idesc | ((uint32_t)(t.n >> 3) << 17);
         for (int kb = kb0; kb < kb1 && ok; ++u) {
-          const int first = kb, end = kSum ? min(kb + kChunk, kb1) : kb1, buf = u & 1;
+          const int first = kb, end = I8 ? kb1 : min(kb + kChunk<TO>, kb1), buf = u & 1;
           ok = u < 2 || role_wait(acc_empty(buf), ((u >> 1) - 1) & 1, status, a.g.wait_ns, aborted);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -550,10 +548,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
         if (ch < a.g.N) ws = a.g.ws[(long long)t.e * a.g.N + ch];
       float xv = split ? 0.f : row_scale(half * 32);
       bool ok = true;
-      if constexpr (kSum) {
+      if constexpr (!I8) {
         constexpr int kParts = kUnitCols / 64;
         uint32_t sum[kParts][32];
-        for (int kb = kb0; kb < kb1; kb += kChunk, ++u) {
+        for (int kb = kb0; kb < kb1; kb += kChunk<TO>, ++u) {
           const int buf = u & 1;
           ok = filled(buf);
           if (!ok) break;

@@ -407,8 +407,9 @@ moe_status_t moe_int8_matmul(const signed char* x, long long x_stride, const flo
 
 /* The same grouped by expert for 16-bit experts: y[r, n] = sum_k x[r, k] *
  * w[e, n, k], fp32 sums, rounded once to y_dtype. (The tensor cores' sums
- * truncate; an fp32 y adds them up every 512 values of K, rounded to nearest.) x and w share dtype (MOE_BF16
- * or MOE_FP16). K <= 2^24; offsets, other limits and strides as above. */
+ * truncate: they are added up, rounded to nearest, every 512 values of K for an
+ * fp32 y, every 1024 for a 16-bit one, so that the error does not grow with K but
+ * for those additions.) x and w share dtype (MOE_BF16 or MOE_FP16). K <= 2^24; offsets, other limits and strides as above. */
 moe_status_t moe_grouped_matmul(const void* x, long long x_stride, const void* w, long long w_stride,
                                 long long expert_stride, const int* offsets, int rows, int experts, int K, int N,
                                 moe_dtype_t dtype, void* y, long long y_stride, moe_dtype_t y_dtype,

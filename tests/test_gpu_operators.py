@@ -436,6 +436,47 @@ def test_grouped_matmul_long_sums(bq, R, N, K):
     assert float((got - ref).norm() / ref.norm()) <= 32 * 2.0 ** -23 * 2 / 3 + U * (K / 512) ** 0.5
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("R,N,K", [(2048, 2048, 14336), (16, 512, 131072), (200, 512, 14335)])
+def test_16_bit_outputs_are_rounded_sums(bq, dtype, R, N, K):
+    """How many 16-bit outputs are not the 64-bit value rounded once. A sum that is
+    off by e rounds otherwise with probability e / step. Accumulators truncate 64
+    times in 1024 values of K, each time by half a unit of 2^-23 on average, which is
+    0.36 * 2^-23 of a partial sum between two powers of two, whose size is on average
+    two thirds of its chunk's; chunks are independent and are added to nearest: e is
+    64 * 0.36 * 2^-23 * 2 / 3 + 2^-24 sqrt(K / 1024) of the outputs' size. Twice the
+    mean of e / step leaves room for the count's own spread. (All of K in one
+    accumulator: 14 times as much at K = 14336.)"""
+    gen = seeded(R, N, K, len(dtype), ord(dtype[0]))
+    x, w = rnd(gen, (R, K), 1.0, DT[dtype]), rnd(gen, (1, N, K), 0.02, DT[dtype])
+    got = bq.moe_grouped_matmul(x, w).double()
+    ref = x.double() @ w[0].double().t()
+    fi = torch.finfo(DT[dtype])
+    step = torch.exp2(torch.floor(torch.log2(ref.abs().clamp_min(fi.smallest_normal)))) * fi.eps
+    off = ((got - ref).abs() > step / 2).double().mean()
+    e = (64 * 0.36 * 2.0 ** -23 * 2 / 3 + U * (K / 1024) ** 0.5) * ref.square().mean().sqrt()
+    assert float(off) <= 2 * float((e / step).clamp_max(1.0).mean()) + 4 / ref.numel()
+
+
+@pytest.mark.parametrize("out", ["fp16", "fp32"])
+@pytest.mark.parametrize("R,N,K", [(64, 256, 131072), (300, 1024, 65536), (1100, 2048, 32768), (3, 200, 131071), (400, 512, 65535)])
+def test_grouped_matmul_sums_do_not_drift(bq, out, R, N, K):
+    """Positive terms, where truncation always takes away: 64 times in 1024 values
+    of K at most 2^-23 of a partial sum, which is no larger than the chunk's: 64 *
+    2^-23 of the output at any K; and K / 512 + 4 additions to nearest, 2^-24 of a
+    partial output each. In one go it would be up to K / 16 * 2^-23."""
+    gen = seeded(R, N, K)
+    x = (torch.rand(R, K, generator=gen) + 0.5).half().cuda()
+    w = (torch.rand(1, N, K, generator=gen) / 1024).half().cuda()
+    got = bq.moe_grouped_matmul(x, w, out_dtype=DT[out]).double()
+    ref = x.double() @ w[0].double().t()
+    tol = (64 * 2.0 ** -23 + (K / 512 + 4) * U) * ref
+    fi = torch.finfo(DT[out])
+    half = torch.exp2(torch.floor(torch.log2(ref + tol))) * fi.eps / 2
+    worst = float(((got - ref).abs() - half).max() / tol.min())
+    assert bool(((got - ref).abs() <= half + tol).all()), worst
+
+
 @pytest.mark.parametrize("out", ["bf16", "fp32"])
 def test_int8_matmul_scales(bq, out):
     gen = seeded(11)
