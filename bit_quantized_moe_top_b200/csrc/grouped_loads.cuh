@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const _
   __shared__ __align__(8) uint64_t bars_s[2 * kStagesLoads + 3];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
+  __shared__ unsigned status_s;  // of this CTA's waits
   constexpr int ES = I8 ? 1 : 2;
   constexpr uint32_t kSums = 128;  // first TMEM column of the sums of a tile's earlier chunks
   constexpr uint32_t kCols = I8 ? kSums : 2 * kSums;
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const _
   const uint32_t acc_full = bars + 8 * (2 * kStagesLoads), acc_empty = acc_full + 8, drained = acc_full + 16;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int* aborted = &abort_s;
-  unsigned* status = &g_op_status;
+  unsigned* status = &status_s;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStagesLoads; ++s) {
       mbar_init(full(s), kLoadWarps);
@@ -96,6 +97,7 @@ __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const _
     mbar_init(acc_empty, kLoadWarps);
     mbar_init(drained, 1);
     abort_s = 0;
+    status_s = 0;
     fence_barrier_init();
   }
   if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), kCols);
@@ -234,4 +236,5 @@ __global__ void __launch_bounds__(kThreadsLoads, 2) grouped_loads_kernel(const _
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, kCols);
+  if (threadIdx.x == 0 && status_s) atomicAdd(&g_op_timeouts, 1u);
 }

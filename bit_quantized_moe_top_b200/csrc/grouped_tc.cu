@@ -24,9 +24,9 @@
 // expert the weights' bytes (128 rows in 8 experts of 4096 x 28672: 307 us, 95%
 // of HBM's rate); with a few rows in all, latency (4.3 us for 2 rows).
 // Roles: warp 0 TMA producer, warp 1 MMA (of the pair's first CTA), warps 2-9
-// epilogue. Every mbarrier wait is bounded; one that runs out sets the status
-// word, every role of the CTA stops at its next wait, the cluster drains its
-// copies and MMAs, frees TMEM and returns.
+// epilogue. Every mbarrier wait is bounded; one that runs out is counted, every
+// role of the CTA stops at its next wait, the cluster drains its copies and MMAs,
+// frees TMEM and returns.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -39,7 +39,7 @@
 
 namespace moeq {
 
-__device__ unsigned g_op_status;
+__device__ unsigned g_op_timeouts;  // CTAs of the products in which a bounded wait ran out; only ever counted up
 
 namespace {
 
@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
   __shared__ __align__(8) uint64_t bars_s[2 * kMaxStagesTc + 6];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s, issued_s;
+  __shared__ unsigned status_s;  // of this CTA's waits
   __shared__ uint32_t bytes_s[kMaxStagesTc];  // of the stage's last copies
   __shared__ uint32_t cluster_abort;
   constexpr int kUnitCols = CG == 2 ? 256 : 128;  // TMEM columns of one accumulator
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
   const int cluster = blockIdx.x / csize, nclusters = gridDim.x / csize;
   const int lead = CG == 2 ? 0 : (int)rank;       // CTA whose MMA warp consumes this CTA's stages
   volatile int* aborted = &abort_s;
-  unsigned* status = &g_op_status;
+  unsigned* status = &status_s;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
@@ -392,6 +393,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
     mbar_init(drained, 1);
     mbar_init(summed, kEpiWarps * (CG == 1 ? a.S : 1));
     abort_s = 0;
+    status_s = 0;
     cluster_abort = 0;
     issued_s = 0;
     fence_barrier_init();
@@ -701,6 +703,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) grouped_tc_kernel(const __grid_
   }
   if (warp == 1) free_tmem<CG>(tmem, kCols);
   if constexpr (CG == 2) cluster_sync();  // the pair's TMEM goes together
+  if (threadIdx.x == 0 && status_s) atomicAdd(&g_op_timeouts, 1u);
 }
 
 // ---------------------------------------------------------------------------
@@ -911,13 +914,9 @@ cudaError_t launch_grouped_loads(const GroupedArgs& g, int op, int y_dtype, cuda
   });
 }
 
-cudaError_t read_op_status(unsigned* out, cudaStream_t st) {
-  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_op_status, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, st);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  const unsigned zero = 0;
-  if (e == cudaSuccess && *out) e = cudaMemcpyToSymbolAsync(g_op_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, st);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  return e;
+cudaError_t read_op_timeouts(unsigned* out, cudaStream_t st) {
+  const cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_op_timeouts, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, st);
+  return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
 }
 
 }  // namespace moeq

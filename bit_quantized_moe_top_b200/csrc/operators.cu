@@ -36,7 +36,50 @@ moe_status_t check_product(const void* x, long long ldx, const void* w, long lon
   return MOE_OK;
 }
 
+// What each stream has been told of its device's count of timeouts. The count only
+// grows and every stream keeps its own place in it, so that no caller takes
+// another's timeout. A stream gets its place with its first product, at the
+// highest count that anyone had read by then (which its calls cannot be part of);
+// one without a place (it only replays graphs, or the table is full) starts at 0
+// and may be told of timeouts before its time, never too few. Streams are known
+// by their handles: asking CUDA for a stream's number ends a capture of it.
+struct Told {
+  std::atomic<unsigned long long> key{0};  // 0: free
+  std::atomic<unsigned> count{0};
+};
+constexpr int kPlaces = 4096;
+Told g_told[kPlaces];
+constexpr int kMaxDevices = 64;
+std::atomic<unsigned> g_read[kMaxDevices];  // highest count read
+
+unsigned long long key_of(cudaStream_t st, int dev) {
+  static std::atomic<unsigned long long> threads{0};
+  static thread_local const unsigned long long thread = ++threads;
+  unsigned long long id = (unsigned long long)reinterpret_cast<uintptr_t>(st);
+  if (st == cudaStreamPerThread) id |= thread << 12;  // another stream in every thread; no other handle ends in its bits
+  return id << 8 | (unsigned)(dev + 1);
+}
+// the stream's place, a new one if make; null if there is none
+Told* place_of(cudaStream_t st, int dev, bool make, unsigned start) {
+  const unsigned long long key = key_of(st, dev);
+  for (int i = 0, h = (int)(key * 0x9E3779B97F4A7C15ull >> 52); i < kPlaces; ++i, h = (h + 1) % kPlaces) {
+    unsigned long long k = g_told[h].key.load(std::memory_order_acquire);
+    if (k == 0) {
+      if (!make) return nullptr;
+      if (g_told[h].key.compare_exchange_strong(k, key)) {
+        g_told[h].count.store(start);
+        return &g_told[h];
+      }
+    }
+    if (k == key) return &g_told[h];
+  }
+  return nullptr;
+}
+
 moe_status_t run_product(GroupedArgs& a, int op, int y_dtype, cudaStream_t st) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return MOE_ERR_CUDA;
+  place_of(st, dev, true, g_read[dev].load());
   a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   return cuda_status(grouped_tc_fits(a, op) ? launch_grouped_tc(a, op, y_dtype, st)
                                             : launch_grouped_loads(a, op, y_dtype, st));
@@ -144,9 +187,16 @@ moe_status_t moe_grouped_matmul(const void* x, long long x_stride, const void* w
 }
 
 moe_status_t moe_op_sync_status(void* cuda_stream) {
-  unsigned s = 0;
-  if (read_op_status(&s, static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) return MOE_ERR_CUDA;
-  return s & ST_TIMEOUT ? MOE_ERR_TIMEOUT : s ? MOE_ERR_DEVICE_CHECK : MOE_OK;
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  unsigned now = 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices || read_op_timeouts(&now, st) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  for (unsigned seen = g_read[dev].load(); seen < now && !g_read[dev].compare_exchange_weak(seen, now);) {
+  }
+  Told* t = place_of(st, dev, now != 0, 0);
+  const unsigned before = t ? t->count.exchange(now) : 0;
+  return now != before ? MOE_ERR_TIMEOUT : MOE_OK;
 }
 
 moe_status_t moe_op_set_wait_limit(unsigned long long limit_ns) {

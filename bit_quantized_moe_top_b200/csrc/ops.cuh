@@ -67,8 +67,8 @@ bool grouped_tc_fits(const GroupedArgs& a, int op);
 cudaError_t launch_grouped_tc(const GroupedArgs& a, int op, int y_dtype, cudaStream_t st);
 // for the calls that do not fit
 cudaError_t launch_grouped_loads(const GroupedArgs& a, int op, int y_dtype, cudaStream_t st);
-// the products' device status word, read and cleared once the stream is idle
-cudaError_t read_op_status(unsigned* out, cudaStream_t st);
+// how many CTAs of the products have given up a wait on the current device, read once the stream is idle
+cudaError_t read_op_timeouts(unsigned* out, cudaStream_t st);
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v);

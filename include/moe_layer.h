@@ -316,10 +316,11 @@ moe_status_t moe_route_topk_noalloc(const float* router_logits, int T, int E, in
  * What a transformer block does next to the expert layer, on the caller's
  * tensors: the norms, gate and residual on both sides of a block, and the
  * products of experts (routed or shared) that are kept at 8 or 16 bits instead
- * of 2-4. None of them allocates device memory, keeps a workspace or state
- * between calls, or uses floating-point atomics: calls on different streams do
- * not interact, every call can be captured into a CUDA graph, and repeated
- * calls give the same bits. All are asynchronous on cuda_stream, whose device
+ * of 2-4. None of them allocates device memory, keeps a workspace between
+ * calls, or uses floating-point atomics: calls on different streams do not
+ * interact, every call can be captured into a CUDA graph, and repeated calls give
+ * the same bits. (Kept are a count of timeouts per device, for
+ * moe_op_sync_status, and the limit of the waits, both for the whole process.) All are asynchronous on cuda_stream, whose device
  * must be the current one and hold every tensor.
  * Strides are in elements; a row's elements are contiguous. A call with no
  * rows returns MOE_OK and launches nothing.
@@ -416,9 +417,13 @@ moe_status_t moe_grouped_matmul(const void* x, long long x_stride, const void* w
                                 void* cuda_stream);
 
 /* Synchronise cuda_stream and return what the products' own device-side checks
- * found on the current device since the last call (MOE_ERR_TIMEOUT: a bounded
- * wait gave up), then clear it; MOE_ERR_CUDA for a pending CUDA error. Call it
- * while no product runs on another stream of the device. */
+ * found on the current device: MOE_ERR_TIMEOUT if a bounded wait of any product
+ * there gave up since this stream was last asked about (or had its first
+ * product), else MOE_OK; MOE_ERR_CUDA for a pending CUDA error. Every stream is
+ * told of every timeout, once, its own and other streams' alike: nobody's answer
+ * takes another's away, and products may run on other streams meanwhile. A
+ * stream that only replays captured products may also be told of timeouts before
+ * its first use. */
 moe_status_t moe_op_sync_status(void* cuda_stream);
 
 /* Limit, in nanoseconds, of the products' waits between roles, for the whole

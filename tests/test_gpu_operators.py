@@ -650,6 +650,69 @@ def test_products_wait_limit_then_recovery(bq, op, R, N, K, pad):
     assert bq.moe_op_sync_status() == 0
 
 
+def test_every_stream_is_told_of_a_timeout(bq):
+    """An answer about one stream takes no other stream's timeout away."""
+    gen = seeded(31)
+    x, w, _, _ = operands("bf16", gen, 700, 1, 2048, 2048)
+    mine, other, idle = (torch.cuda.Stream() for _ in range(3))
+    call = lambda st: bq.moe_grouped_matmul(x, w, stream=st.cuda_stream)
+    torch.cuda.synchronize()
+    for st in (mine, other, idle):
+        want = call(st)
+        bq.moe_op_sync_status(st.cuda_stream)
+    assert all(bq.moe_op_sync_status(st.cuda_stream) == 0 for st in (mine, other, idle))
+    bq.moe_op_set_wait_limit(1)
+    try:
+        for _ in range(5):
+            call(mine)
+            mine.synchronize()
+            if bq.moe_op_sync_status(other.cuda_stream) == 8:
+                break
+    finally:
+        bq.moe_op_set_wait_limit(0)
+    # the stream whose call it was, the others, and the current one: each once
+    for st in (mine.cuda_stream, idle.cuda_stream, torch.cuda.current_stream().cuda_stream):
+        assert bq.moe_op_sync_status(st) == 8
+    for st in (mine, other, idle, torch.cuda.current_stream()):
+        assert bq.moe_op_sync_status(st.cuda_stream) == 0
+    assert torch.equal(call(mine), want)
+    assert bq.moe_op_sync_status(mine.cuda_stream) == 0
+    # a stream whose first product comes after a timeout is not told of it
+    late = torch.cuda.Stream(priority=-1)
+    call(late)
+    assert bq.moe_op_sync_status(late.cuda_stream) == 0
+
+
+def test_timeout_of_a_replayed_product(bq):
+    """Captured on one stream, replayed on another: both are told."""
+    gen = seeded(32)
+    x, w, _, _ = operands("int8", gen, 8, 1, 256, 4096)[:4]
+    xs, ws = torch.ones(8, device="cuda"), torch.ones(1, 256, device="cuda")
+    bq.moe_int8_matmul(x, xs, w, ws)
+    here, there = torch.cuda.current_stream(), torch.cuda.Stream()
+    with torch.cuda.stream(there):
+        bq.moe_int8_matmul(x, xs, w, ws)
+    for st in (here, there):
+        bq.moe_op_sync_status(st.cuda_stream)
+        assert bq.moe_op_sync_status(st.cuda_stream) == 0
+    g = torch.cuda.CUDAGraph()
+    bq.moe_op_set_wait_limit(1)
+    try:
+        with torch.cuda.graph(g):
+            bq.moe_int8_matmul(x, xs, w, ws)
+    finally:
+        bq.moe_op_set_wait_limit(0)
+    told = 0
+    for _ in range(5):
+        with torch.cuda.stream(there):
+            g.replay()
+        told = bq.moe_op_sync_status(there.cuda_stream)
+        if told:
+            break
+    assert told == 8 and bq.moe_op_sync_status(here.cuda_stream) == 8
+    assert bq.moe_op_sync_status(there.cuda_stream) == bq.moe_op_sync_status(here.cuda_stream) == 0
+
+
 # ---------------------------------------------------------------------------
 # streams, graphs and the calls together
 # ---------------------------------------------------------------------------
