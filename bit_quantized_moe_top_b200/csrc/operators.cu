@@ -32,7 +32,9 @@ moe_status_t check_product(const void* x, long long ldx, const void* w, long lon
   if (!offsets && E != 1) return MOE_ERR_INVALID_ARG;
   if (ldx < 0 || ldw < 0 || ldwe < 0 || (rows > 1 && ldy < N)) return MOE_ERR_INVALID_ARG;
   if (rows > 0 && (!x || !w || !y)) return MOE_ERR_INVALID_ARG;
-  if (!at_elements(x, es) || !at_elements(w, es) || !at_elements(y, yd == MOE_FP32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
+  if (!at_elements(x, es) || !at_elements(w, es) || !at_elements(y, yd == MOE_FP32 ? 4 : 2) ||
+      !at_elements(offsets, 4))
+    return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
@@ -111,7 +113,7 @@ moe_status_t moe_block_norm(const moe_block_norm_t* p, void* cuda_stream) {
   const int rs = p->residual_dtype == MOE_FP32 ? 4 : 2;
   if (!at_elements(p->branch, 2) || !at_elements(p->post_weight, 2) || !at_elements(p->gate, 2) ||
       !at_elements(p->pre_weight, 2) || !at_elements(p->h, 2) || !at_elements(p->residual, rs) ||
-      !at_elements(p->residual_out, rs))
+      !at_elements(p->residual_out, rs) || !at_elements(p->inv_pos, 4) || !at_elements(p->pair_weights, 4))
     return MOE_ERR_INVALID_ARG;
   if (p->tokens == 0) return MOE_OK;
   NormArgs a{};
@@ -151,7 +153,7 @@ moe_status_t moe_quantize_rows(const void* x, long long x_stride, int x_rows, mo
     return MOE_ERR_INVALID_ARG;
   if (width > kMaxRowWidth) return MOE_ERR_TOO_LARGE;
   if (rows > 0 && ((!x && x_rows > 0) || !codes || !scales)) return MOE_ERR_INVALID_ARG;
-  if (!at_elements(x, 2)) return MOE_ERR_INVALID_ARG;
+  if (!at_elements(x, 2) || !at_elements(src_rows, 4) || !at_elements(scales, 4)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
   QuantArgs a{x, x_stride, x_rows, src_rows, rows, width, codes, codes_stride, scales};
   return cuda_status(launch_quantize_rows(a, dtype, static_cast<cudaStream_t>(cuda_stream)));
@@ -166,6 +168,7 @@ moe_status_t moe_int8_matmul(const signed char* x, long long x_stride, const flo
   if (s != MOE_OK) return s;
   if (K > 131071) return MOE_ERR_TOO_LARGE;
   if (rows > 0 && (!row_scales || !channel_scales)) return MOE_ERR_INVALID_ARG;
+  if (!at_elements(row_scales, 4) || !at_elements(channel_scales, 4)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
   GroupedArgs a{x, x_stride, w, w_stride, expert_stride, row_scales, channel_scales, offsets, rows, experts, K, N,
                 y, y_stride, 0};

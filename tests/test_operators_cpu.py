@@ -164,6 +164,21 @@ def test_pointers_off_their_elements_are_refused(bq):
     assert lib.moe_int8_matmul(P, 64, P, P, 64, 0, P, None, 4, 1, 64, 32, P + 2, 32, bq.FP32, None) == INVALID
 
 
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_words_off_their_boundary_are_refused(bq, off):
+    """Indices, offsets and scales of 4 bytes too: a misaligned one would fault on the device."""
+    lib, Q = bq._lib(), P + off
+    for name in ("inv_pos", "pair_weights"):
+        kw = {"pairs": 2, "inv_pos": P, "pair_weights": P, name: Q}
+        assert _norm(bq, **kw) == INVALID
+    assert _quant(bq, src=Q) == INVALID
+    assert _quant(bq, s=Q) == INVALID
+    for int8 in (False, True):
+        assert _mm(bq, int8, off=Q) == INVALID
+    assert _mm(bq, True, xs=Q) == INVALID
+    assert _mm(bq, True, ws=Q) == INVALID
+
+
 def test_product_extents(bq):
     lib = bq._lib()
     big = (1 << 29) + 1
