@@ -13,6 +13,7 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmoeq.so")
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_STAMP = os.path.join(HERE, "_binding.stamp")  # what the binding was built against
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["moe_layer.cu", "route.cu", "relayout.cu", "decode_gemm.cu", "lowrank.cu", "noalloc.cu", "prefill_gemm.cu",
@@ -44,8 +45,23 @@ def _newer(out, deps) -> bool:
     return os.path.exists(out) and all(os.path.getmtime(d) <= os.path.getmtime(out) for d in deps)
 
 
+def _binding_key() -> str:
+    """The torch and the Python whose headers and ABI the binding takes."""
+    import sysconfig
+
+    import torch
+    return f"torch {torch.__version__} cxx11 {int(torch.compiled_with_cxx11_abi())} {sysconfig.get_config_var('SOABI')}"
+
+
+def _binding_current() -> bool:
+    if not os.path.exists(BINDING_STAMP) or not _newer(BINDING, _binding_inputs()):
+        return False
+    with open(BINDING_STAMP) as f:
+        return f.read() == _binding_key()
+
+
 def up_to_date() -> bool:
-    return _newer(LIB, _inputs()[1]) and _newer(BINDING, _binding_inputs())
+    return _newer(LIB, _inputs()[1]) and _binding_current()
 
 
 def build_binding() -> str:
@@ -66,6 +82,8 @@ def build_binding() -> str:
     if r.returncode != 0:
         raise RuntimeError(f"binding failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_binding_key())
     return BINDING
 
 
@@ -74,7 +92,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
         return LIB
     if force or not _newer(LIB, _inputs()[1]):
         build_library(verbose, ptxas_v)
-    if force or not _newer(BINDING, _binding_inputs()):
+    if force or not _binding_current():
         build_binding()
     return LIB
 
