@@ -1,5 +1,6 @@
-"""Build the in-tree CUDA library ``libmoeq.so`` for sm_100a with nvcc, and the
-binding of the operators to torch tensors with the host compiler."""
+"""Build the in-tree CUDA library ``libmoeq.so`` for sm_100a with nvcc, and, where
+torch with CUDA is installed, the binding of the operators to torch tensors with the host
+compiler. The library alone serves the C ABI."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -53,7 +54,17 @@ def _binding_key() -> str:
     return f"torch {torch.__version__} cxx11 {int(torch.compiled_with_cxx11_abi())} {sysconfig.get_config_var('SOABI')}"
 
 
+def _have_torch() -> bool:
+    try:
+        import torch
+    except ImportError:
+        return False
+    return torch.version.cuda is not None
+
+
 def _binding_current() -> bool:
+    if not _have_torch():
+        return True  # nothing to bind to
     if not os.path.exists(BINDING_STAMP) or not _newer(BINDING, _binding_inputs()):
         return False
     with open(BINDING_STAMP) as f:
@@ -92,7 +103,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
         return LIB
     if force or not _newer(LIB, _inputs()[1]):
         build_library(verbose, ptxas_v)
-    if force or not _binding_current():
+    if _have_torch() and (force or not _binding_current()):
         build_binding()
     return LIB
 

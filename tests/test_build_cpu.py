@@ -36,3 +36,18 @@ def test_binding_of_another_python_is_rebuilt(built, monkeypatch):
     assert not build.up_to_date()
     build.build()
     assert built == [1]
+
+
+def test_library_without_torch(built, monkeypatch, tmp_path):
+    """The C ABI needs nvcc alone: without torch there is no binding to build or to miss."""
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_binding.so"))
+    monkeypatch.setitem(sys.modules, "torch", None)  # import torch raises ImportError
+    assert build.up_to_date()
+    assert build.build() == build.LIB and build.build(force=False) == build.LIB
+    assert not built
+
+
+def test_library_beside_a_torch_without_cuda(built, monkeypatch, tmp_path):
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(torch.version, "cuda", None)
+    assert build.up_to_date() and build.build() == build.LIB and not built
