@@ -96,9 +96,11 @@ moe_status_t moe_block_norm(const moe_block_norm_t* p, void* cuda_stream) {
       (p->residual_dtype != MOE_FP32 && p->residual_dtype != p->dtype))
     return MOE_ERR_INVALID_ARG;
   if (p->width > kMaxRowWidth) return MOE_ERR_TOO_LARGE;
-  if ((!p->branch && !p->residual) || (!p->residual_out && !p->h) || !p->h != !p->pre_weight)
+  const bool no_rows = p->pairs > 0 && p->branch_rows == 0;  // every pair is dropped: there may be no branch to point to
+  const bool branch = p->branch || no_rows;
+  if ((!branch && !p->residual) || (!p->residual_out && !p->h) || !p->h != !p->pre_weight)
     return MOE_ERR_INVALID_ARG;
-  if (!p->branch && (p->pairs || p->post_weight || p->gate)) return MOE_ERR_INVALID_ARG;
+  if (!branch && (p->pairs || p->post_weight || p->gate)) return MOE_ERR_INVALID_ARG;
   if (p->pairs < 0 || p->pairs > kMaxTopK || (p->pairs > 0 && (!p->inv_pos || !p->pair_weights || p->branch_rows < 0)) ||
       (p->pairs == 0 && p->branch && p->branch_rows < p->tokens))
     return MOE_ERR_INVALID_ARG;

@@ -334,7 +334,8 @@ typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype_t;
  * the combination of the experts' rows. Per token t, in fp32 throughout:
  *   b  = branch[t]                                        (pairs = 0)
  *      = sum_j pair_weights[t, j] * branch[inv_pos[t, j]] (pairs > 0, in slot
- *        order; an inv_pos outside [0, branch_rows) adds nothing: a dropped pair)
+ *        order; an inv_pos outside [0, branch_rows) adds nothing: a dropped pair;
+ *        with branch_rows = 0 branch may be NULL)
  *   n  = b * rsqrt(mean(b^2) + eps) * (weight_offset + post_weight)   (post_weight set, else n = b)
  *   r' = residual_scale * residual[t] + branch_scale * g * n
  *   h  = r' * rsqrt(mean(r'^2) + eps) * (weight_offset + pre_weight)  (pre_weight set)

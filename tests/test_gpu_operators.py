@@ -192,6 +192,18 @@ def test_block_norm_forms(bq):
     assert empty_r.shape == (0, 256) and empty_h.shape == (0, 256)
 
 
+@pytest.mark.parametrize("T,K,post", [(1, 4096, True), (300, 256, False), (7, 2051, True)])
+def test_block_norm_without_branch_rows(bq, T, K, post):
+    """No expert had a row: every pair is dropped, and the branch adds nothing."""
+    y, r, kw = norm_case(bq, T, K, "bf16", "bf16", k=3, gate="channel", post=post)
+    kw["inv_pos"] = (torch.arange(3 * T, dtype=torch.int32).reshape(T, 3) - 1).cuda()
+    none = y[:0].clone()
+    got_r, got_h = bq.moe_block_norm(r, none, **kw)
+    ref, h, tol_r, tol_h = norm_reference(r, none, kw)
+    check(got_r, ref, tol_r + half_step(torch.bfloat16, ref), "residual")
+    check(got_h, h, tol_h + half_step(torch.bfloat16, h), "h")
+
+
 def test_block_norm_broadcast_rows(bq):
     """One residual row for every token (stride 0)."""
     y, r, kw = norm_case(bq, 9, 128, "fp16", "fp16")
