@@ -109,6 +109,14 @@ PyObject* guarded(const char* where, Body body) {
   }
   END_HANDLE_TH_ERRORS
 }
+// a tensor that the call wrote into: a change in place, as autograd counts them
+PyObject* written(PyObject* o) {
+  if (given(o)) {
+    const at::Tensor& t = tensor(o);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  }
+  return o;
+}
 PyObject* keep(PyObject* o) {
   Py_INCREF(o);
   return o;
@@ -216,7 +224,8 @@ PyObject* block_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
       a.h = h.data_ptr();
     }
     if (T > 0) run([&] { return moe_block_norm(&a, place.stream()); });
-    return pair(r.defined() ? THPVariable_Wrap(r) : keep(residual_out), h.defined() ? THPVariable_Wrap(h) : keep(h_out));
+    return pair(r.defined() ? THPVariable_Wrap(r) : keep(written(residual_out)),
+                h.defined() ? THPVariable_Wrap(h) : keep(written(h_out)));
   });
 }
 
@@ -254,7 +263,8 @@ PyObject* quantize_rows(PyObject*, PyObject* const* args, Py_ssize_t n) {
       return moe_quantize_rows(x.data_ptr(), ldx, m, (moe_dtype_t)code_of(x.scalar_type()), src, rows, width,
                                static_cast<signed char*>(q.data_ptr()), ldq, scales, place.stream());
     });
-    return pair(given(args[2]) ? keep(args[2]) : THPVariable_Wrap(q), given(args[3]) ? keep(args[3]) : THPVariable_Wrap(s));
+    return pair(given(args[2]) ? keep(written(args[2])) : THPVariable_Wrap(q),
+                given(args[3]) ? keep(written(args[3])) : THPVariable_Wrap(s));
   });
 }
 
@@ -311,7 +321,7 @@ PyObject* int8_matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
                              static_cast<const signed char*>(w.data_ptr()), p.ldw, p.ldwe, ws, p.offsets, p.rows, p.experts,
                              p.K, p.N, p.y.data_ptr(), p.ldy, p.type(), place.stream());
     });
-    return given(args[6]) ? keep(args[6]) : THPVariable_Wrap(p.y);
+    return given(args[6]) ? keep(written(args[6])) : THPVariable_Wrap(p.y);
   });
 }
 
@@ -327,7 +337,7 @@ PyObject* grouped_matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
       return moe_grouped_matmul(x.data_ptr(), p.ldx, w.data_ptr(), p.ldw, p.ldwe, p.offsets, p.rows, p.experts, p.K, p.N,
                                 (moe_dtype_t)code_of(x.scalar_type()), p.y.data_ptr(), p.ldy, p.type(), place.stream());
     });
-    return given(args[4]) ? keep(args[4]) : THPVariable_Wrap(p.y);
+    return given(args[4]) ? keep(written(args[4])) : THPVariable_Wrap(p.y);
   });
 }
 

@@ -632,6 +632,32 @@ def test_block_norm_refused_forms(bq):
         assert ei.value.status == 1
 
 
+def test_written_tensors_raise_their_version(bq):
+    """What a call writes into a given tensor is a change in place: a backward pass that saved it notices."""
+    x = torch.randn(8, 64, device="cuda").bfloat16()
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    W = torch.zeros(32, 64, dtype=torch.bfloat16, device="cuda")
+    r, h, y = torch.empty_like(x), torch.empty_like(x), torch.empty(8, 32, dtype=torch.bfloat16, device="cuda")
+    q, s = torch.empty(8, 64, dtype=torch.int8, device="cuda"), torch.empty(8, device="cuda")
+    z = torch.empty(8, 32, device="cuda")
+    before = [t._version for t in (x, r, h, y, q, s, z)]
+    bq.moe_block_norm(x, x, w_pre=w, residual_out=r, h_out=h)
+    bq.moe_quantize_rows(x, codes=q, scales=s)
+    bq.moe_grouped_matmul(x, W, out=y)
+    bq.moe_int8_matmul(q, s, W.to(torch.int8), torch.ones(32, device="cuda"), out=z)
+    assert [t._version - b for t, b in zip((x, r, h, y, q, s, z), before)] == [0, 1, 1, 1, 1, 1, 1]
+    a = torch.ones(8, 32, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    loss = (a * y).sum()
+    bq.moe_grouped_matmul(x, W, out=y)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        out = torch.empty(8, 32, dtype=torch.bfloat16, device="cuda")
+        bq.moe_grouped_matmul(x, W, out=out)
+    bq.moe_grouped_matmul(x, W, out=out)  # an inference tensor has no version
+    assert torch.equal(out, y)
+
+
 @pytest.mark.parametrize("op", ["bf16", "int8"])
 @pytest.mark.parametrize("R,N,K,pad", [
     (700, 2048, 2048, 0),    # CTA pairs
