@@ -19,7 +19,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["moe_layer.cu", "route.cu", "relayout.cu", "decode_gemm.cu", "lowrank.cu", "noalloc.cu", "prefill_gemm.cu",
            "planner.cpp", "tileq.cu", "block_norm.cu", "grouped_tc.cu", "operators.cu"]
-HEADERS = ["common.cuh", "decode_frag.cuh", "tc.cuh", "kernels.h", "ops.cuh", "grouped_loads.cuh"]
+HEADERS = ["common.cuh", "decode_frag.cuh", "tc.cuh", "kernels.h", "ops.cuh", "grouped_loads.cuh", "grouped_form.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]

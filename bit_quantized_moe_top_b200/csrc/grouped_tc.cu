@@ -33,6 +33,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "grouped_form.h"
 #include "kernels.h"
 #include "ops.cuh"
 #include "tc.cuh"
@@ -220,17 +221,14 @@ __device__ __forceinline__ Tile tile_of(const GroupTable& g, const TcArgs& a, in
   return t;
 }
 
-// The tiles of the last, incomplete turn of the persistent pairs go to two or
-// four of them each, by rows, where that many are free: half a tile takes about
-// three quarters of its time (4095 x 7168 x 4096, 256 tiles on 74 pairs, 8-bit
-// 80 -> 75 us; 9000 x 4096 x 1792 in 4 experts, 16-bit 99 -> 95 us).
+// A pair's work: whole tiles, then its share of the last turn's.
 template <int CG>
 struct Turns {
   int whole, parts, items;  // tiles of complete turns; parts of each further one; all pieces of work
   __device__ __forceinline__ Turns(int tiles, int clusters) {
     const int rest = CG == 2 ? tiles % clusters : 0;
     whole = tiles - rest;
-    parts = rest * 4 <= clusters ? 4 : rest * 2 <= clusters ? 2 : 1;
+    parts = last_turn_parts(rest, clusters);
     items = whole + rest * parts;
   }
 };
@@ -840,49 +838,7 @@ cudaError_t launch_grouped_tc(const GroupedArgs& g, int op, int y_dtype, cudaStr
   const long long ldx = g.rows > 1 ? g.ldx : (g.K + 15) / 16 * 16;
   const long long ldwe = g.E > 1 ? g.ldwe : g.ldw * g.N;
   const int nk = (g.K * es + kRowBytes - 1) / kRowBytes;
-  // Tile width and form, by an estimate of cycles. Groups are taken as equally
-  // large (their sizes are only known on the device). Per 128 bytes of K a CTA
-  // needs the larger of its MMAs, 2 cycles a row, and its L2 reads of 128
-  // channels and the rows it copies, at 60 bytes a cycle or its share of 6600 of
-  // all (8192 x 4096 x 4096 reads 12.5 TB/s). So narrower tiles cost nearly as
-  // much as wide ones, and it is the number of tiles that a CTA works off one
-  // after the other that counts. The split of K (CG = 1) pays an exchange of the
-  // partial sums, about 1500 cycles and 55 a column, a pair about 300 to set up.
-  // Clusters of eight are left out: not all of those that would fill the SMs find
-  // room at once (1 x 7168 x 2048 17.0 us, four 10.6). Over 38 sizes of 1 to 2000
-  // rows the choice took at most 10% more than the best of all forms, 2% on average.
-  const int groups = std::min(g.rows, g.E), mean = (g.rows - 1) / groups + 1;
-  const int nf[3] = {0, (g.N - 1) / 128 + 1, (g.N - 1) / 256 + 1};  // channel tiles by CG
-  const double streamed = (double)groups * g.N * nk * (kRowBytes / 3500.0);  // weights at HBM's bytes per cycle
-  auto cost_of = [&](int cg, int width, int S) {
-    const int nt = (mean - 1) / width + 1, unit = 16 * cg;
-    const int n = ((mean - 1) / nt / unit + 1) * unit;
-    const int tiles = groups * nt * nf[cg], slots = cg == 2 ? pairs : sms / S, waves = (tiles - 1) / slots + 1;
-    const double rate = std::min(60.0, 6600.0 / (cg * S * std::min(tiles, slots)));
-    const int loaded = (n / cg + kBoxRows - 1) / kBoxRows * kBoxRows;
-    const double per_k = std::max(2.0 * n, (128 + loaded) * kRowBytes / rate) + 0.1 * n;  // fewer MMAs where reads bound both
-    return std::max(waves * per_k * ((nk - 1) / S + 1), streamed) + (S > 1 ? 1500 + 55 * n : 0) + (cg == 2 ? 300 : 0);
-  };
-  int cg = 2, width = 256, S = 1;
-  double best = cost_of(2, 256, 1);
-  auto consider = [&](int c, int w, int s) {
-    const double cost = cost_of(c, w, s);
-    if (cost < best) {
-      best = cost;
-      cg = c;
-      width = w;
-      S = s;
-    }
-  };
-  for (int w = 224; w >= 64; w -= 32)
-    if (mean > w - 32) consider(2, w, 1);  // a narrower tile holds the rest
-  // few tiles: single CTAs, split along K while there are CTAs for it
-  for (int w = 128; w >= 16; w /= 2) {
-    if (mean <= w / 2 && w > 16) continue;
-    const int tiles = groups * nf[1] * ((mean - 1) / w + 1);
-    for (int s = 1; s <= 4 && tiles * s <= sms; s *= 2)
-      if (s == 1 || nk >= s * 2) consider(1, w, s);
-  }
+  const auto [cg, width, S] = choose_form(g.rows, g.E, g.N, (long long)g.K * es, sms);
   TcArgs a = common_args(g, op, cg, width);
   a.S = S;
   const long long most = most_tiles(g, a.nmax, a.NF);

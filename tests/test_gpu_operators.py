@@ -21,6 +21,7 @@ import pytest
 import torch
 
 from oracle import operators as orc
+from product_forms import FORMS
 
 pytestmark = pytest.mark.gpu
 
@@ -390,6 +391,15 @@ def test_products_tile_forms(bq, op, counts, N, K, opt):
     """Sizes over the range in which the tiles' width and the split of K change."""
     run_exact(bq, op, "fp32", counts, N, K, **opt)
     run_exact(bq, op, "bf16", counts, N, K, **opt)
+
+
+@pytest.mark.parametrize("op,counts,N,K", [f[:4] for f in FORMS])
+def test_every_form_of_the_products(bq, op, counts, N, K):
+    """Every tile width, split of K and sharing of the last turn that some size takes, into 32 and 16 bits."""
+    if torch.cuda.get_device_properties(0).multi_processor_count != 148:
+        pytest.skip("the forms are listed for 148 SMs")
+    run_exact(bq, op, "fp32", counts, N, K)
+    run_exact(bq, op, "bf16" if op == "int8" else op, counts, N, K)
 
 
 @pytest.mark.parametrize("seed", range(12))
