@@ -75,3 +75,26 @@ def test_null_handles_are_rejected(bq):
     assert lib.moe_layer_last_launch_count(None) == 0
     assert lib.moe_layer_create(4, 256, 256, 8, 2, None, 0, None) == 1
     lib.moe_layer_destroy(None)
+
+
+def test_block_norm_arguments_lie_as_in_the_header(bq, tmp_path):
+    """The ctypes structure and the header's have the same fields at the same offsets."""
+    import subprocess
+    names = [n for n, _ in bq.BlockNormArgs._fields_]
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    body = re.search(r"typedef struct \{([^}]*)\} moe_block_norm_t;", text).group(1)
+    assert re.findall(r"(\w+)\s*(?=[,;])", body) == names
+    src = tmp_path / "offsets.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "moe_layer.h"\nint main(void) {\n'
+                   + "".join(f'  printf("%zu %zu\\n", offsetof(moe_block_norm_t, {n}), sizeof(((moe_block_norm_t*)0)->{n}));\n'
+                             for n in names)
+                   + '  printf("%zu\\n", sizeof(moe_block_norm_t));\n  return 0;\n}\n')
+    exe = tmp_path / "offsets"
+    subprocess.run([os.environ.get("CC", "gcc"), "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
+    got = [int(v) for v in out]
+    want = []
+    for n in names:
+        f = getattr(bq.BlockNormArgs, n)
+        want += [f.offset, f.size]
+    assert got == want + [ctypes.sizeof(bq.BlockNormArgs)]

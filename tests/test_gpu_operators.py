@@ -458,6 +458,19 @@ def test_grouped_matmul_long_sums(bq, R, N, K):
     assert float((got - ref).norm() / ref.norm()) <= 32 * 2.0 ** -23 * 2 / 3 + U * (K / 512) ** 0.5
 
 
+@pytest.mark.parametrize("R,N,K", [(8, 512, 8192), (300, 1024, 8192), (3, 200, 7168)])
+def test_grouped_matmul_long_sums_of_a_split(bq, R, N, K):
+    """fp32 outputs where four CTAs split K, each summing some 2048 values of it. A
+    chunk's 32 truncations take half a unit of 2^-23 each, on average 0.36 * 2^-23 of
+    a partial sum that is two thirds of the chunk's: 32 * 0.36 * 2^-23 * 2 / 3, and
+    the roundings to nearest of the chunks. 2048 values in one go: four times that."""
+    gen = seeded(R, N, K)
+    x, w = rnd(gen, (R, K), 1.0, torch.float16), rnd(gen, (1, N, K), 0.02, torch.float16)
+    got = bq.moe_grouped_matmul(x, w, out_dtype=torch.float32).double()
+    ref = x.double() @ w[0].double().t()
+    assert float((got - ref).norm() / ref.norm()) <= 32 * 0.36 * 2.0 ** -23 * 2 / 3 + U * (K / 512) ** 0.5
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("R,N,K", [(2048, 2048, 14336), (16, 512, 131072), (200, 512, 14335)])
 def test_16_bit_outputs_are_rounded_sums(bq, dtype, R, N, K):
@@ -595,6 +608,57 @@ def test_products_repeat_bitwise(bq, op, R):
     first = product(bq, op, x, w, off, torch.float32, xs, ws)
     for _ in range(5):
         assert torch.equal(product(bq, op, x, w, off, torch.float32, xs, ws), first)
+
+
+FAR = 2 ** 30 + 256  # elements between rows: the third row lies beyond 2^31
+
+
+@pytest.fixture
+def far_rows():
+    """Three rows of a matrix that spans more than 2^31 elements, at column c."""
+    raw = torch.empty(2 * (2 * FAR + 4096), dtype=torch.uint8, device="cuda")
+    yield lambda c, width, dtype: raw.view(dtype).as_strided((3, width), (FAR, 1), c)
+    del raw
+    torch.cuda.empty_cache()
+
+
+def test_rows_beyond_2_31_elements(bq, far_rows):
+    gen = seeded(41)
+    put = lambda c, t: far_rows(c, t.shape[1], t.dtype).copy_(t)
+    y, r, kw = norm_case(bq, 3, 256, "bf16", "bf16", k=1, gate="element")
+    y = y[:3].contiguous()
+    kw["inv_pos"] = torch.tensor([[2], [0], [1]], dtype=torch.int32).cuda()
+    want = bq.moe_block_norm(r, y, **kw)
+    kw["gate"] = put(0, kw["gate"])
+    got = bq.moe_block_norm(put(256, r), put(512, y), residual_out=far_rows(768, 256, torch.bfloat16),
+                            h_out=far_rows(1024, 256, torch.bfloat16), **kw)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    src = torch.tensor([2, 0, 1], dtype=torch.int32).cuda()
+    want = bq.moe_quantize_rows(r, src)
+    got = bq.moe_quantize_rows(far_rows(256, 256, torch.bfloat16), src, codes=far_rows(4000, 256, torch.int8))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("op", ["fp16", "int8"])
+@pytest.mark.parametrize("shift", [0, 1])  # bulk copies, ordinary loads
+def test_products_beyond_2_31_elements(bq, far_rows, op, shift):
+    gen = seeded(42, shift)
+    x, w, xs, ws = operands(op, gen, 3, 1, 160, 256)
+    want = product(bq, op, x, w, None, torch.float32, xs, ws)
+    far = far_rows(64 + shift, 256, x.dtype).copy_(x)
+    y = far_rows(1024, 160, torch.float16)
+    got = product(bq, op, far, w, None, torch.float16, xs, ws, y)
+    assert torch.equal(got, want.half())
+    # experts that far apart: the third one's rows
+    x, w, xs, ws = operands(op, gen, 7, 3, 1, 256)
+    off = split([2, 0, 5])
+    want = product(bq, op, x, w, off, torch.float32, xs, ws)
+    rows = far_rows(64 + shift, 256, x.dtype)
+    rows.copy_(w[:, 0])
+    apart = rows[:, None, :]
+    got = product(bq, op, x, apart, off, torch.float32, xs, ws)
+    assert torch.equal(got, want)
+    assert bq.moe_op_sync_status() == 0
 
 
 def test_refusals_on_the_device(bq):
