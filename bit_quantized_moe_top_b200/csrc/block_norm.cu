@@ -187,8 +187,13 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : NV == 4 && FORM == kShift ? 5
     block_norm_kernel(const __grid_constant__ NormArgs a) {
   constexpr bool SHIFT = FORM == kShift;
   __shared__ float red[2][4 * 32];
-  constexpr int kAhead = SHIFT ? 1 : NV == 1 ? 4 : 2;  // combined rows in flight
-  constexpr int kGroup = SHIFT && NV == 4 ? 2 : NV;           // vectors of a row in flight
+  // Combined rows in flight, as many as the registers hold. One, two, four, eight,
+  // us: 128 x 7168 with eight rows (NV = 1) 10.0, 8.5, 7.8, 8.2; 8192 x 4096 with
+  // two (NV = 2) 69, 62, 74; shifted 1027 x 2051 with eight 21.7, 23.0, 40.
+  constexpr int kAhead = SHIFT ? 1 : NV == 1 ? 4 : 2;
+  // Vectors of a row in flight: all, but half of the four of shifted rows, whose
+  // loads take twice the registers (4096 x 9001 with two rows 133 us, all four 258).
+  constexpr int kGroup = SHIFT && NV == 4 ? 2 : NV;
   constexpr bool kLate = kGroup < NV;
   pdl_wait();
   pdl_trigger();

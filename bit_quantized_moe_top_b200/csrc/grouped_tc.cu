@@ -51,7 +51,11 @@ constexpr int kABytes = 128 * kRowBytes;       // 128 channels
 constexpr int kBoxRows = 32;                   // unit of the rows per TMA box of x
 constexpr int kBoxBytes = kBoxRows * kRowBytes;
 constexpr int kMaxStagesTc = 10;
-constexpr int kBandTc = 8;                     // row tiles that share a sweep over the channels
+// Row tiles that share a sweep over the channels: few re-read the weights, many
+// the rows. One, four, eight, sixteen, thirty-two, us: 8192 x 4096 x 8192 386,
+// 360, 352, 350, 388; 16384 x 14336 x 4096 1283, 1284, 1276, 1326, 1441; 2048 x
+// 4096 x 28672 398, 317, 305, 305, 303.
+constexpr int kBandTc = 8;
 constexpr int kStagingBytes = kEpiWarps * 2048;
 
 // The tensor cores add to their fp32 accumulators with truncation, whose error
