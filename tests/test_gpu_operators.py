@@ -976,3 +976,71 @@ def test_operators_captured(bq):
             want = chain(bq, s)[0]
             assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1])
     assert bq.moe_op_sync_status() == 0
+
+
+FIRST_CALLS = """
+import threading
+import torch
+import bit_quantized_moe_top_b200 as bq
+
+torch.manual_seed(0)
+x = torch.randn(40, 256, device="cuda").bfloat16()
+w = torch.randn(2, 128, 256, device="cuda").bfloat16()
+one = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+off = torch.tensor([0, 15, 40], dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+
+
+def calls(x):
+    _, h = bq.moe_block_norm(x, w_pre=one)
+    q, s = bq.moe_quantize_rows(h)
+    wq, ws = bq.moe_quantize_rows(w.reshape(-1, 256))
+    y = bq.moe_int8_matmul(q, s, wq.reshape(2, 128, 256), ws.reshape(2, 128), off)
+    return [h, q, s, y, bq.moe_grouped_matmul(h, w, off), bq.moe_grouped_matmul(h[:, 1:], w[:, :, 1:], off)]
+
+
+def captured():
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = calls(x)
+    g.replay()
+    return [out]
+
+
+def threads():
+    out = [None] * 4
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            out[i] = calls(x)
+            torch.cuda.current_stream().synchronize()
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    return out
+
+
+first = MODE()
+torch.cuda.synchronize()
+want = calls(x)
+torch.cuda.synchronize()
+for got in first:
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+assert bq.moe_op_sync_status() == 0
+print("the same")
+"""
+
+
+@pytest.mark.parametrize("mode", ["captured", "threads"])
+def test_first_calls_of_a_process(bq, mode):
+    """Nothing has to be called once beforehand: the first calls may be captured, or made by several threads at once."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.replace("MODE", mode)], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "the same" in r.stdout, r.stderr[-2000:]
