@@ -9,8 +9,12 @@
 // pairs of fp32 values (one instruction for two), and rows are split into 8
 // elements per thread and vector even where no row starts at a 16-byte
 // boundary. Measured, of HBM's 6.46 TB/s: norm of 16384 x 2048 95%, 8192 x 4096
-// with two combined rows 84%, 4000 x 14336 67%, 1027 x 2051 35%; quantiser of
-// 8192 x 4096 99%, 16384 x 14336 95%.
+// with two combined rows 83%; quantiser of 8192 x 4096 97%, 16384 x 14336 94%.
+// Rows of more than 8192 elements take 110 to 124 registers a thread, so that one
+// row at a time lives on an SM and HBM idles through its two reductions: norm of
+// 4000 x 14336 67%. Rows at any alignment take two loads and a shift for every
+// vector, the norms' weights among them, anew for each row: norm of 1027 x 2051
+// 33%, 4096 x 9001 50%; quantiser of 8192 x 4095 60%, 4000 x 14335 60%.
 #include "kernels.h"
 #include "ops.cuh"
 

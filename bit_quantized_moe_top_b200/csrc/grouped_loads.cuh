@@ -12,8 +12,8 @@
 // pieces around them, or read element by element where those would leave the row.
 // A tile's sums of earlier chunks wait in TMEM, beside the accumulators. Bound by
 // the loads' latency, which two CTAs of three stages cover in part: 16384 rows by
-// 4096 channels of 14335 in 8 experts 7.8 ms (bulk copies at 14336: 1.38), 8-bit
-// 4.0 (0.65); one row of 2047 by 2816 channels 47 us, 8-bit 29.
+// 4096 channels of 14335 in 8 experts 7.7 ms (bulk copies at 14336: 1.26), 8-bit
+// 4.0 (0.59); one row of 2047 by 2816 channels 47 us, 8-bit 29.
 
 constexpr int kLoadWarps = 8;
 constexpr int kThreadsLoads = 32 * kLoadWarps;

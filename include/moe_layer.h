@@ -313,6 +313,11 @@ moe_status_t moe_route_topk_noalloc(const float* router_logits, int T, int E, in
                                     float* w, int* counts, int* offsets, void* cuda_stream);
 
 /* ---- Stand-alone operators around the experts ----
+ * (The expert order of a batch, for src_rows and inv_pos, is a stable sort of the
+ * (token, slot) pairs by the idx that moe_route_topk_noalloc writes, as its
+ * offsets count them: sorted pair i belongs to token perm_token[i], and pair (t, j)
+ * lies at inv_pos[t, j]. That call does not write the two arrays; the caller's
+ * own sort makes them, or moe_layer_get_routing after a forward of a layer.)
  * What a transformer block does next to the expert layer, on the caller's
  * tensors: the norms, gate and residual on both sides of a block, and the
  * products of experts (routed or shared) that are kept at 8 or 16 bits instead
@@ -377,7 +382,7 @@ moe_status_t moe_block_norm(const moe_block_norm_t* args, void* cuda_stream);
 
 /* Activations to 8 bits, one scale per row: with a = max|x[s]|,
  *   scales[i] = a / 127,  codes[i, c] = round_half_even(127 * x[s, c] / a),
- * s = src_rows[i] (the gather into expert order, e.g. perm_token) or i when
+ * s = src_rows[i] (the gather into expert order) or i when
  * src_rows is NULL (then rows = x_rows). The codes are the exact roundings of
  * the quotient. A row of zeros, and a src_rows entry outside [0, x_rows), gives
  * codes 0 with scale 0; a row that holds a NaN or an infinity gives codes 0
@@ -391,7 +396,8 @@ moe_status_t moe_quantize_rows(const void* x, long long x_stride, int x_rows, mo
 /* Products of 8-bit integers, scaled per row and per output channel, grouped
  * by expert: for the rows r of expert e, offsets[e] <= r < offsets[e + 1],
  *   y[r, n] = row_scales[r] * channel_scales[e, n] * sum_k x[r, k] * w[e, n, k]
- * with exact int32 sums, scaled in fp32 and rounded once to y_dtype.
+ * with exact int32 sums, scaled in fp32 (by the two scales' product) and rounded
+ * once to y_dtype.
  * offsets: int32 [experts + 1] on the device, ascending within [0, rows] (as
  * moe_route_topk_noalloc writes them), or NULL with experts = 1 (all rows).
  * An expert may have no rows; rows outside every expert's range are left as
@@ -399,9 +405,10 @@ moe_status_t moe_quantize_rows(const void* x, long long x_stride, int x_rows, mo
  * maximum clamped to [0, rows].
  * x int8 [rows, K], w int8 [experts, N, K], channel_scales fp32 [experts, N],
  * y [rows, N] of y_dtype. K <= 131071 (int32 sums), experts <= 256, rows and
- * N <= 2^29, else MOE_ERR_TOO_LARGE. Pointers and strides of x and w that are not multiples of
- * 16 bytes, and rows that overlap, which bulk copies cannot address, take a
- * kernel with ordinary loads, four to seven times slower. */
+ * N <= 2^29, else MOE_ERR_TOO_LARGE. Pointers and strides of x and w that are not
+ * multiples of 16 bytes, rows that overlap, and an expert_stride that is no
+ * multiple of w_stride, which bulk copies cannot address, take a kernel with
+ * ordinary loads, four to six times slower. */
 moe_status_t moe_int8_matmul(const signed char* x, long long x_stride, const float* row_scales, const signed char* w,
                              long long w_stride, long long expert_stride, const float* channel_scales,
                              const int* offsets, int rows, int experts, int K, int N, void* y, long long y_stride,
